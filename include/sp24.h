@@ -391,6 +391,92 @@ SP24_API sp24_status sp24_flip_rate(const uint8_t *idx_prev, const uint8_t *idx_
                            unsigned long long *d_count, void *stream);
 
 /*
+ * Orthogonalisation of update matrices by Newton-Schulz products, as the Muon
+ * optimiser does (K. Jordan et al., 2024), next to the gradient operations
+ * below: for each of `count` matrices G [rows x cols],
+ *   X <- G / (|G|_F + eps);  steps times:  A = X X^T,  X <- a X + (b A + c A^2) X
+ * with (a, b, c) = (3.4445, -4.7750, 2.0315), on G^T when rows > cols; out = X.
+ * Singular values of G that are not far below the largest end near 1 (between
+ * 0.68 and 1.13 after five steps).
+ *   G    device fp32, count matrices batch_stride elements apart, row-major
+ *        with leading dimension ldg >= cols (as the weight gradients above)
+ *   out  device dtype [count][rows][cols] contiguous, overwritten
+ *   steps 1..16; eps >= 0
+ *   workspace  device, sp24_orthogonalize_size() bytes, 16-byte aligned; its
+ *        contents do not matter and are not kept.  One call uses it at a time:
+ *        calls that may overlap (streams, graphs replayed side by side) take
+ *        one each.
+ * Any rows, cols >= 0, the shorter one at most 65536; a zero-sized call does
+ * nothing.  A zero matrix gives zeros; a NaN or infinity anywhere in a matrix
+ * makes its whole result NaN.  The norm is summed in fp64; the iterates are fp16
+ * (scaled by a power of two near sqrt of the longer side) with fp32
+ * accumulation, about 1e-3 relative error of the result for gradients whose
+ * large singular directions do not dwarf the others (the error grows in
+ * proportion to |G|_2 over the typical entry of the rest).
+ * G and out need only their types' alignment (a matrix of a stack of any size).
+ */
+SP24_API sp24_status sp24_orthogonalize_size(int64_t count, int64_t rows, int64_t cols, size_t *workspace_bytes);
+SP24_API sp24_status sp24_orthogonalize(const float *G, int64_t count, int64_t rows, int64_t cols, int64_t ldg,
+                               int64_t batch_stride, int steps, float eps, void *out, sp24_dtype dtype,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One Muon step of `count` weights of one shape, all in one call: momentum,
+ * orthogonalisation as sp24_orthogonalize, decoupled weight decay and update of
+ * the fp32 weight, and the 16-bit copy that sp24_mask_step and the products read:
+ *   momentum <- mu momentum + grad
+ *   U = grad + mu momentum (nesterov != 0), or momentum
+ *   W <- (1 - lr weight_decay) W - lr scale NS(U);   W16 <- round(W)
+ *   grad, momentum, W  device fp32 [count][rows][cols] contiguous (grad is only
+ *        read: the output of sp24_gemm_wgrad_decay or sp24_masked_decay)
+ *   W16  device dtype [count][rows][cols], or NULL
+ * The update is added to W in the last product's epilogue, from its fp32
+ * accumulator.  Hyperparameters are values of the call (a captured graph keeps
+ * them).  A NaN or infinity in U makes that weight NaN.  Sizes, steps, eps,
+ * workspace and alignment as for sp24_orthogonalize.
+ */
+SP24_API sp24_status sp24_muon_step(const float *grad, float *momentum, float *W, void *W16, sp24_dtype dtype,
+                           int64_t count, int64_t rows, int64_t cols, float mu, int nesterov, float lr,
+                           float weight_decay, float scale, int steps, float eps, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/*
+ * 8-bit quantisation of the rows of a 16-bit matrix (tokens of activations, or
+ * output channels of a weight), the operands of sp24_gemm_i8:
+ *   scale[r] = amax_r / 127,  q[r][c] = rint(x[r][c] * (127 * (1 / amax_r)))
+ * with amax_r = max |x[r][c]| over the row, in IEEE fp32 operations rounding to
+ * nearest even.  With idx, the matrix is a weight W and its masked form is
+ * quantised: pruned entries count as 0, whatever they hold.
+ *   X      device dtype [rows x ldx], ldx >= cols, 16-byte aligned
+ *   idx    device uint8 [rows/4][cols/4] (sp24_mask_search; rows, cols multiples
+ *          of 4), or NULL
+ *   q      device int8 [rows x cols] contiguous, 16-byte aligned
+ *   scale  device fp32 [rows]
+ * A row of zeros, or one whose amax is below 2^-100, gives scale 0 and q 0; a row
+ * with a NaN or infinity (in a kept place) gives scale NaN and q 0.  rows,
+ * cols >= 0 (cols == 0: scales of 0).
+ */
+SP24_API sp24_status sp24_quantize_rows(const void *X, sp24_dtype dtype, int64_t rows, int64_t cols, int64_t ldx,
+                               const uint8_t *idx, int8_t *q, float *scale, void *stream);
+
+/*
+ * 8-bit forward product with a scale for each token and each output channel, the
+ * inference counterpart of sp24_gemm_fwd / sp24_gemm_dense:
+ *   Y[t][n] = (sum_k Xq[t][k] Wq[n][k]) * sw[n] * sx[t],  optionally gelu of it
+ * The sum is exact (32-bit integers); then two fp32 products in that order, the
+ * GELU (exact erf form) in fp32, and one rounding to dtype.
+ *   Xq  device int8 [T x K], sx device fp32 [T] (sp24_quantize_rows of X)
+ *   Wq  device int8 [N x K], sw device fp32 [N] (of W, or of W with its mask)
+ *   Y   device dtype [T x N], overwritten
+ *   epi SP24_EPI_NONE or SP24_EPI_GELU (no aux here: nothing is saved for a
+ *       backward pass)
+ * All row-major and contiguous.  K % 16 == 0, N % 16 == 0, K <= 131056 (where the
+ * sum cannot overflow), T >= 0.  Xq, Wq and Y 16-byte aligned.
+ */
+SP24_API sp24_status sp24_gemm_i8(const int8_t *Xq, const float *sx, int64_t T, int64_t K, const int8_t *Wq,
+                         const float *sw, int64_t N, sp24_dtype dtype, void *Y, sp24_epilogue epi, void *stream);
+
+/*
  * Maps the device metadata of an [rows x cols] matrix compressed along its
  * rows (meta_bytes from sp24_compressed_size) to the canonical form: for row
  * r, group g (columns 4g..4g+3) with kept offsets i0 < i1, the nibble

@@ -28,6 +28,7 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 P, I64, I32, U64, F32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64, ctypes.c_float
+SZ = ctypes.c_size_t
 _SIGNATURES = {
     "sp24_pattern_table": [P],
     "sp24_mask_search": [P, I32, I64, I64, I64, P, P],
@@ -51,6 +52,11 @@ _SIGNATURES = {
     "sp24_aux_pack": [P, I64, I64, P],
     "sp24_aux_unpack": [P, I64, I64, P],
     "sp24_meta_from_canonical": [P, I64, I64, P],
+    "sp24_orthogonalize_size": [I64, I64, I64, P],
+    "sp24_orthogonalize": [P, I64, I64, I64, I64, I64, I32, F32, P, I32, P, SZ, P],
+    "sp24_muon_step": [P, P, P, P, I32, I64, I64, I64, F32, I32, F32, F32, F32, I32, F32, P, SZ, P],
+    "sp24_quantize_rows": [P, I32, I64, I64, I64, P, P, P, P],
+    "sp24_gemm_i8": [P, P, I64, I64, P, P, I64, I32, P, I32, P],
     "sp24_device_status": [P],
     "sp24_set_wait_budget": [U64],
 }
@@ -443,6 +449,122 @@ def sp24_flip_rate(idx_prev, idx_cur, count, stream=None):
     _need_device(idx_prev, idx_cur, count)
     _check("sp24_flip_rate",
            _lib.sp24_flip_rate(_ptr(idx_prev), _ptr(idx_cur), idx_cur.numel(), _ptr(count), _stream(stream)))
+
+
+def _one_device(*ts):
+    """The CUDA device that all of `ts` (None allowed) live on."""
+    _need_device(*ts)
+    devices = {t.device for t in ts if t is not None}
+    if len(devices) != 1:
+        raise ValueError(f"sp24 takes tensors of one device, got {sorted(map(str, devices))}")
+    return devices.pop()
+
+
+def _call_on(device, fn: str, stream, *args):
+    """Calls the entry point with `device` current, on `stream` or that device's current stream."""
+    import torch
+    with torch.cuda.device(device):
+        _check(fn, getattr(_lib, fn)(*args, _stream(stream)))
+
+
+def _stack3(t, name: str):
+    """(count, rows, cols) of a matrix or a stack of matrices."""
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name}: expected a matrix or a stack of matrices, got {t.dim()}-D")
+    return (1, *t.shape) if t.dim() == 2 else tuple(t.shape)
+
+
+def _out_code(t, name: str) -> int:
+    import torch
+    if t.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    return _dtype_code(t)
+
+
+def sp24_orthogonalize_size(rows: int, cols: int, count: int = 1) -> int:
+    """Workspace bytes of sp24_orthogonalize and sp24_muon_step for `count` [rows, cols] matrices."""
+    out = ctypes.c_size_t(0)
+    _check("sp24_orthogonalize_size", _lib.sp24_orthogonalize_size(count, rows, cols, ctypes.byref(out)))
+    return out.value
+
+
+def sp24_orthogonalize(G, out, workspace, steps: int = 5, eps: float = 1e-7, stream=None):
+    """out (fp16/bf16, G's shape) <- Newton-Schulz orthogonalisation of G (fp32 [R, C], or a stack
+    [count, R, C]; rows may be pitched).  workspace: uint8, sp24_orthogonalize_size(R, C, count) bytes,
+    used by one call at a time."""
+    import torch
+    count, R, C = _stack3(G, "G")
+    if C > 1 and G.stride(-1) != 1:
+        raise ValueError("sp24 takes row-major matrices with unit stride along rows")
+    _need_rowmajor(out, workspace)
+    _expect(G, "G", torch.float32, count * R * C)
+    code = _out_code(out, "out")
+    _expect(out, "out", out.dtype, count * R * C)
+    _expect(workspace, "workspace", torch.uint8, sp24_orthogonalize_size(R, C, count))
+    device = _one_device(G, out, workspace)
+    ld = G.stride(-2) if R > 1 else C
+    if ld < C:
+        raise ValueError("sp24 takes row-major matrices with unit stride along rows")
+    batch = G.stride(0) if G.dim() == 3 and count > 1 else R * C
+    _call_on(device, "sp24_orthogonalize", stream, _ptr(G), count, R, C, ld, batch, int(steps), float(eps), _ptr(out),
+             code, _ptr(workspace), workspace.numel())
+
+
+def sp24_muon_step(grad, momentum, W, W16, workspace, lr: float, mu: float = 0.95, nesterov: bool = True,
+                   weight_decay: float = 0.0, scale: float = 1.0, steps: int = 5, eps: float = 1e-7, stream=None):
+    """One Muon step in place: momentum <- mu momentum + grad; W <- (1 - lr weight_decay) W - lr scale NS(U) with
+    U = grad + mu momentum (nesterov) or momentum; W16 (fp16/bf16, or None) <- W.  grad, momentum and W are
+    fp32 [R, C] or stacks [count, R, C]; workspace as for sp24_orthogonalize."""
+    import torch
+    count, R, C = _stack3(W, "W")
+    _need_rowmajor(grad, momentum, W, W16, workspace)
+    for t, name in ((W, "W"), (grad, "grad"), (momentum, "momentum")):
+        _expect(t, name, torch.float32, count * R * C)
+        if t.shape != W.shape:
+            raise ValueError(f"{name}: expected shape {tuple(W.shape)}, got {tuple(t.shape)}")
+    code = SP24_F16 if W16 is None else _out_code(W16, "W16")
+    if W16 is not None:
+        _expect(W16, "W16", W16.dtype, count * R * C)
+    _expect(workspace, "workspace", torch.uint8, sp24_orthogonalize_size(R, C, count))
+    device = _one_device(grad, momentum, W, W16, workspace)
+    _call_on(device, "sp24_muon_step", stream, _ptr(grad), _ptr(momentum), _ptr(W), _ptr(W16), code, count, R, C,
+             float(mu), int(bool(nesterov)), float(lr), float(weight_decay), float(scale), int(steps), float(eps),
+             _ptr(workspace), workspace.numel())
+
+
+def sp24_quantize_rows(X, q, scale, idx=None, stream=None):
+    """q[R, C] (int8), scale[R] (fp32) <- X [R, C] (fp16/bf16, row pitch allowed), a scale amax/127 a row; with
+    idx [R/4, C/4] (uint8) X is a weight and the entries its mask prunes count as 0."""
+    import torch
+    _need_rowmajor(q, scale, idx, pitched=(X,))
+    R, C = _shape2(X, "X")
+    code = _dtype_code(X)
+    _expect(q, "q", torch.int8, R * C)
+    _expect(scale, "scale", torch.float32, R)
+    _expect(idx, "idx", torch.uint8, (R // 4) * (C // 4))
+    device = _one_device(X, q, scale, idx)
+    _call_on(device, "sp24_quantize_rows", stream, _ptr(X), code, R, C, X.stride(0) if R > 1 else C, _ptr(idx), _ptr(q),
+             _ptr(scale))
+
+
+def sp24_gemm_i8(Xq, sx, Wq, sw, Y, epi=None, stream=None):
+    """Y[T, N] (fp16/bf16) <- (Xq[T, K] Wq[N, K]^T) * sw[N] * sx[T] on int8 operands (sp24_quantize_rows);
+    epi None or 'gelu'."""
+    import torch
+    _need_rowmajor(Xq, sx, Wq, sw, Y)
+    T, K = _shape2(Xq, "Xq")
+    N, K2 = _shape2(Wq, "Wq")
+    if K2 != K:
+        raise ValueError(f"Wq has {K2} columns, Xq has {K}")
+    _expect(Xq, "Xq", torch.int8, T * K)
+    _expect(Wq, "Wq", torch.int8, N * K)
+    _expect(sx, "sx", torch.float32, T)
+    _expect(sw, "sw", torch.float32, N)
+    code = _out_code(Y, "Y")
+    _expect(Y, "Y", Y.dtype, T * N)
+    device = _one_device(Xq, sx, Wq, sw, Y)
+    _call_on(device, "sp24_gemm_i8", stream, _ptr(Xq), _ptr(sx), T, K, _ptr(Wq), _ptr(sw), N, code, _ptr(Y),
+             EPILOGUES[epi])
 
 
 def sp24_device_status(stream=None) -> int:

@@ -2,7 +2,7 @@
 //
 // Every entry point validates its arguments on the host first (nothing is
 // launched when a check fails), then enqueues its kernels on the caller's
-// stream.  Nothing here allocates device memory.
+// stream.  Device memory is allocated only for the weight gradient's split-tail workspace.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -14,9 +14,12 @@
 #include <utility>
 
 #include "sp24.h"
+#include "gemm_nt.cuh"
 #include "gemm_sp.cuh"
 #include "mask_kernels.cuh"
 #include "mvue.cuh"
+#include "ortho.cuh"
+#include "quant.cuh"
 
 namespace {
 
@@ -26,6 +29,7 @@ std::atomic<uint64_t> g_wait_budget{1ull << 32};
 
 inline cudaStream_t as_stream(void *s) { return reinterpret_cast<cudaStream_t>(s); }
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned_to(const void *p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 inline bool valid_dtype(sp24_dtype d) { return d == SP24_F16 || d == SP24_BF16; }
 
 sp24_status check_device() {
@@ -534,6 +538,270 @@ sp24_status launch_wgrad(const void *X, int64_t T, int64_t K, const void *A, con
                                                      fixed);
 }
 
+// ------------------------------------------- orthogonalisation and 8-bit products
+
+// 3-D map over [batch][outer][inner] (pitches in bytes).
+bool make_map_3d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t outer, uint64_t batch,
+                 uint64_t pitch_bytes, uint64_t batch_bytes, uint32_t box_inner, uint32_t box_outer,
+                 CUtensorMapSwizzle swizzle, CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT16) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {inner, outer, batch};
+  cuuint64_t strides[2] = {pitch_bytes, batch_bytes};
+  cuuint32_t box[3] = {box_inner, box_outer, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, type, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// CTA pairs of an instantiation that fit at once (and, once per device, its shared-memory opt-in).
+template <int MODE, int BN, bool BF16, bool GELU>
+int nt_pairs() {
+  constexpr int smem_bytes = NtGeom<MODE, BN>::kSmem;
+  auto kernel = sp24_gemm_nt_kernel<MODE, BN, BF16, GELU>;
+  static PerDevice cache;
+  const int dev = current_device();
+  if (dev < 0) return -1;
+  std::call_once(cache.once[dev], [&] {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes) != cudaSuccess) {
+      cudaGetLastError();
+      cache.value[dev] = 0;
+      return;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (unsigned)(sm_count() / 2));
+    cfg.blockDim = dim3(kNtThreads);
+    cfg.dynamicSmemBytes = smem_bytes;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();
+      n = sm_count() / 2;
+    }
+    cache.value[dev] = n;
+  });
+  return cache.value[dev];
+}
+
+template <int MODE, int BN, bool BF16 = false, bool GELU = false>
+sp24_status launch_nt(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &to, NtArgs args,
+                      cudaStream_t stream) {
+  using G = NtGeom<MODE, BN>;
+  const int pairs = nt_pairs<MODE, BN, BF16, GELU>();
+  if (pairs <= 0) return pairs == 0 ? SP24_ERR_CUDA : SP24_ERR_NO_DEVICE;
+  const int64_t tiles = G::kSym ? nt_sym_tiles(args.M, BN)
+                                : ((int64_t)(args.M + 255) / 256) * (((int64_t)args.N + BN - 1) / BN);
+  if (tiles * args.batch > INT32_MAX) return SP24_ERR_UNSUPPORTED_SHAPE;
+  args.tiles = (int)tiles;
+  args.wait_budget = g_wait_budget.load();
+  const int64_t total = tiles * args.batch;
+  const int grid = (int)(total < pairs ? total : pairs);
+  return launch_pdl(sp24_gemm_nt_kernel<MODE, BN, BF16, GELU>, dim3(2 * grid), dim3(kNtThreads), G::kSmem, stream, ta,
+                    tb, to, args);
+}
+
+// Newton-Schulz on the short side m of every matrix, n the long side; the workspace holds the
+// norm's partial sums, two iterates [count][m][ldx], G and P [count][m][ldm] (fp16).
+struct OrthPlan {
+  int64_t count, rows, cols, m, n, ldx, ldm;
+  size_t part, x0, x1, gram, poly, total;   // byte offsets
+  bool tall;
+};
+
+// SP24_ERR_INVALID_ARG / UNSUPPORTED_SHAPE for sizes the call does not take.
+sp24_status orth_plan(int64_t count, int64_t rows, int64_t cols, OrthPlan *p) {
+  if (count < 0 || rows < 0 || cols < 0) return SP24_ERR_INVALID_ARG;
+  if (count > 65535 || rows > (1 << 24) || cols > (1 << 24)) return SP24_ERR_UNSUPPORTED_SHAPE;
+  p->count = count;
+  p->rows = rows;
+  p->cols = cols;
+  p->tall = rows > cols;
+  p->m = p->tall ? cols : rows;
+  p->n = p->tall ? rows : cols;
+  if (p->m > 65536) return SP24_ERR_UNSUPPORTED_SHAPE;
+  p->ldx = (p->n + 7) / 8 * 8;
+  p->ldm = (p->m + 7) / 8 * 8;
+  size_t at = 0;
+  auto take = [&at](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  const size_t bx = (size_t)count * p->m * p->ldx * 2, bm = (size_t)count * p->m * p->ldm * 2;
+  p->part = take((size_t)count * kOrthMaxBlocks * sizeof(double));
+  p->x0 = take(bx);
+  p->x1 = take(bx);
+  p->gram = take(bm);
+  p->poly = take(bm);
+  p->total = at;
+  return SP24_OK;
+}
+
+// The quintic Newton-Schulz coefficients of the Muon optimiser (K. Jordan et al., 2024).
+constexpr float kNsA = 3.4445f, kNsB = -4.7750f, kNsC = 2.0315f;
+
+struct OrthOut {
+  uint16_t *out16;   // Orth: the result; Muon: the 16-bit weight, or null
+  float *w;          // Muon: the fp32 weight
+  float keep, step;
+  bool bf16;
+};
+
+template <bool BF16>
+sp24_status launch_orth_last(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &to, const NtArgs &args,
+                             cudaStream_t s) {
+  return args.w ? launch_nt<kNtMuon, 256, BF16>(ta, tb, to, args, s) : launch_nt<kNtOrth, 256, BF16>(ta, tb, to, args, s);
+}
+
+sp24_status run_orth(const OrthPlan &pl, OrthSrc src, const OrthOut &o, int steps, float eps, void *workspace,
+                     cudaStream_t stream) {
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  double *part = reinterpret_cast<double *>(ws + pl.part);
+  __half *xb[2] = {reinterpret_cast<__half *>(ws + pl.x0), reinterpret_cast<__half *>(ws + pl.x1)};
+  void *gram = ws + pl.gram, *poly = ws + pl.poly;
+  const uint64_t px = (uint64_t)pl.ldx * 2, pm = (uint64_t)pl.ldm * 2;
+  const uint64_t m = (uint64_t)pl.m, n = (uint64_t)pl.n, bt = (uint64_t)pl.count;
+  const CUtensorMapSwizzle s128 = CU_TENSOR_MAP_SWIZZLE_128B, s64 = CU_TENSOR_MAP_SWIZZLE_64B;
+  constexpr int kSymBN = 128, kApplyBN = 256;
+  // x_rows: X as a K-major operand; x_half: the same with a CTA's half of the columns' tile;
+  // x_cols: X as the MN-major operand; *_st: 32 x 32 store tiles.
+  CUtensorMap x_rows[2], x_half[2], x_cols[2], x_st[2], g_rows, g_half, g_st, p_rows, p_st, out_st;
+  bool ok = true;
+  for (int i = 0; i < 2; ++i)
+    ok = ok && make_map_3d(&x_rows[i], xb[i], n, m, bt, px, m * px, 64, 128, s128) &&
+         make_map_3d(&x_half[i], xb[i], n, m, bt, px, m * px, 64, kSymBN / 2, s128) &&
+         make_map_3d(&x_cols[i], xb[i], n, m, bt, px, m * px, 64, 64, s128) &&
+         make_map_3d(&x_st[i], xb[i], n, m, bt, px, m * px, 32, 32, s64);
+  ok = ok && make_map_3d(&g_rows, gram, m, m, bt, pm, m * pm, 64, 128, s128) &&
+       make_map_3d(&g_half, gram, m, m, bt, pm, m * pm, 64, kSymBN / 2, s128) &&
+       make_map_3d(&g_st, gram, m, m, bt, pm, m * pm, 32, 32, s64) &&
+       make_map_3d(&p_rows, poly, m, m, bt, pm, m * pm, 64, 128, s128) &&
+       make_map_3d(&p_st, poly, m, m, bt, pm, m * pm, 32, 32, s64);
+  if (!ok) return SP24_ERR_CUDA;
+  const uint64_t out_row = (uint64_t)pl.cols * 2;
+  const bool tma_out = !o.w && out_row % 16 == 0 && aligned16(o.out16);
+  out_st = p_st;   // not used unless tma_out
+  if (tma_out && !make_map_3d(&out_st, o.out16, (uint64_t)pl.cols, (uint64_t)pl.rows, bt, out_row, out_row * pl.rows, 32,
+                              32, s64))
+    return SP24_ERR_CUDA;
+
+  // Scale of the iterate: a power of two near sqrt(n) (gemm_nt.cuh).
+  int e = 0;
+  while ((int64_t(1) << (2 * (e + 1))) <= pl.n) ++e;
+  const float s = (float)(1 << e);
+
+  const bool vec = src.ld == src.cols && src.stride == src.rows * src.cols && (src.rows * src.cols) % 4 == 0 &&
+                   aligned16(src.g) && (!src.m || aligned16(src.m));
+  const int64_t entries = pl.m * pl.n;
+  int64_t blocks = (entries + 16 * kOrthThreads - 1) / (16 * kOrthThreads);
+  const int64_t cap = 4 * (int64_t)sm_count() / pl.count;
+  if (blocks > cap) blocks = cap < 1 ? 1 : cap;
+  if (blocks > kOrthMaxBlocks) blocks = kOrthMaxBlocks;
+  const dim3 grid1((unsigned)blocks, (unsigned)pl.count);
+  sp24_status st = vec ? launch_pdl(orth_sumsq_kernel<true>, grid1, dim3(kOrthThreads), 0, stream, src, part)
+                       : launch_pdl(orth_sumsq_kernel<false>, grid1, dim3(kOrthThreads), 0, stream, src, part);
+  if (st != SP24_OK) return st;
+  const int64_t row_tiles = (pl.rows + kOrthTile - 1) / kOrthTile;
+  const dim3 grid2((unsigned)((pl.cols + kOrthTile - 1) / kOrthTile), (unsigned)(row_tiles < 65535 ? row_tiles : 65535),
+                   (unsigned)pl.count);
+  st = pl.tall ? launch_pdl(orth_scale_kernel<true>, grid2, dim3(kOrthThreads), 0, stream, src, part, (int)blocks, s, eps,
+                            xb[0], pl.ldx, row_tiles)
+               : launch_pdl(orth_scale_kernel<false>, grid2, dim3(kOrthThreads), 0, stream, src, part, (int)blocks, s, eps,
+                            xb[0], pl.ldx, row_tiles);
+  if (st != SP24_OK) return st;
+
+  NtArgs base = {};
+  base.M = (int)pl.m;
+  base.batch = (int)pl.count;
+  base.a = kNsA;
+  base.b = kNsB;
+  base.c = kNsC;
+  base.gram = static_cast<const uint16_t *>(gram);
+  base.gram_ld = pl.ldm;
+  for (int k = 0; k < steps; ++k) {
+    const int in = k & 1;
+    NtArgs a = base;
+    a.N = (int)pl.m;
+    a.num_kt = (int)((pl.n + 63) / 64);
+    a.alpha = 1.0f / (s * s);
+    if ((st = launch_nt<kNtGram, kSymBN>(x_rows[in], x_half[in], g_st, a, stream)) != SP24_OK) return st;
+    a.num_kt = (int)((pl.m + 63) / 64);
+    if ((st = launch_nt<kNtPoly, kSymBN>(g_rows, g_half, p_st, a, stream)) != SP24_OK) return st;
+    a.N = (int)pl.n;
+    if (k + 1 < steps) {
+      st = launch_nt<kNtApply, kApplyBN>(p_rows, x_cols[in], x_st[1 - in], a, stream);
+    } else {
+      a.out16 = o.out16;
+      a.w = o.w;
+      a.keep = o.keep;
+      a.alpha = (o.w ? o.step : 1.0f) / s;
+      a.tall = pl.tall ? 1 : 0;
+      a.tma_out = tma_out ? 1 : 0;
+      a.vec = !pl.tall && pl.n % 2 == 0 && aligned_to(o.w, 8) && aligned_to(o.out16, 4) ? 1 : 0;
+      st = o.bf16 ? launch_orth_last<true>(p_rows, x_cols[in], out_st, a, stream)
+                  : launch_orth_last<false>(p_rows, x_cols[in], out_st, a, stream);
+    }
+    if (st != SP24_OK) return st;
+  }
+  return SP24_OK;
+}
+
+sp24_status validate_orth(const OrthPlan &pl, int steps, float eps, const void *workspace, size_t workspace_bytes) {
+  if (steps < 1 || steps > 16 || !(eps >= 0.0f)) return SP24_ERR_INVALID_ARG;
+  if (pl.count == 0 || pl.m == 0) return SP24_OK;
+  if (!workspace) return SP24_ERR_INVALID_ARG;
+  if (!aligned16(workspace)) return SP24_ERR_MISALIGNED;
+  if (workspace_bytes < pl.total) return SP24_ERR_SCRATCH_TOO_SMALL;
+  return SP24_OK;
+}
+
+// Longest contraction whose 32-bit integer sum cannot overflow: K 128 128 <= 2^31 - 1, K a
+// multiple of 16.
+constexpr int64_t kMaxI8K = 131056;
+
+template <bool BF16, bool GELU>
+sp24_status launch_i8(const int8_t *Xq, int64_t T, int64_t K, const int8_t *Wq, int64_t N, void *Y, const float *sx,
+                      const float *sw, cudaStream_t s) {
+  const CUtensorMapSwizzle s128 = CU_TENSOR_MAP_SWIZZLE_128B;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  NtArgs a = {};
+  a.M = (int)N;
+  a.N = (int)T;
+  a.num_kt = (int)((K + 127) / 128);
+  a.batch = 1;
+  a.row_scale = sw;
+  a.col_scale = sx;
+  const int64_t mt = (N + 255) / 256;
+  const int bn = mt * ((T + 255) / 256) >= sm_count() / 2 ? 256 : (T > 64 ? 128 : 64);
+  CUtensorMap ta, tb, to;
+  if (!make_map_3d(&ta, Wq, (uint64_t)K, (uint64_t)N, 1, (uint64_t)K, (uint64_t)K * N, 128, 128, s128, u8) ||
+      !make_map_3d(&tb, Xq, (uint64_t)K, (uint64_t)T, 1, (uint64_t)K, (uint64_t)K * T, 128, (uint32_t)(bn / 2), s128, u8) ||
+      !make_map_3d(&to, Y, (uint64_t)N, (uint64_t)T, 1, (uint64_t)N * 2, (uint64_t)N * T * 2, 32, 32,
+                   CU_TENSOR_MAP_SWIZZLE_64B))
+    return SP24_ERR_CUDA;
+  switch (bn) {
+    case 256: return launch_nt<kNtI8, 256, BF16, GELU>(ta, tb, to, a, s);
+    case 128: return launch_nt<kNtI8, 128, BF16, GELU>(ta, tb, to, a, s);
+    default: return launch_nt<kNtI8, 64, BF16, GELU>(ta, tb, to, a, s);
+  }
+}
+
+template <bool BF16>
+sp24_status launch_quant(const uint16_t *X, int64_t rows, int64_t cols, int64_t ldx, const uint8_t *idx, int8_t *q,
+                         float *scale, cudaStream_t s) {
+  const unsigned grid = (unsigned)(rows < INT32_MAX ? rows : INT32_MAX);
+  return idx ? launch_pdl(quantize_rows_kernel<BF16, true>, dim3(grid), dim3(kQuantThreads), 0, s, X, rows, cols, ldx, idx,
+                          q, scale)
+             : launch_pdl(quantize_rows_kernel<BF16, false>, dim3(grid), dim3(kQuantThreads), 0, s, X, rows, cols, ldx,
+                          idx, q, scale);
+}
+
 }  // namespace
 
 namespace {
@@ -829,6 +1097,107 @@ sp24_status sp24_flip_rate(const uint8_t *idx_prev, const uint8_t *idx_cur, int6
   const int64_t want = (nblocks / 16 + 255) / 256 + 1;
   const int grid = (int)(want < (int64_t)sm_count() * 8 ? want : (int64_t)sm_count() * 8);
   return launch_pdl(flip_count_kernel, dim3(grid), dim3(256), 0, s, idx_prev, idx_cur, nblocks, d_count);
+}
+
+sp24_status sp24_orthogonalize_size(int64_t count, int64_t rows, int64_t cols, size_t *workspace_bytes) {
+  if (!workspace_bytes) return SP24_ERR_INVALID_ARG;
+  OrthPlan pl;
+  const sp24_status st = orth_plan(count, rows, cols, &pl);
+  if (st != SP24_OK) return st;
+  *workspace_bytes = pl.total;
+  return SP24_OK;
+}
+
+sp24_status sp24_orthogonalize(const float *G, int64_t count, int64_t rows, int64_t cols, int64_t ldg,
+                               int64_t batch_stride, int steps, float eps, void *out, sp24_dtype dtype,
+                               void *workspace, size_t workspace_bytes, void *stream) {
+  OrthPlan pl;
+  sp24_status st = orth_plan(count, rows, cols, &pl);
+  if (st != SP24_OK) return st;
+  if (ldg < cols || batch_stride < 0) return SP24_ERR_INVALID_ARG;
+  if (!valid_dtype(dtype)) return SP24_ERR_UNSUPPORTED_DTYPE;
+  if ((st = validate_orth(pl, steps, eps, workspace, workspace_bytes)) != SP24_OK) return st;
+  const bool empty = count == 0 || pl.m == 0;
+  if (!empty && (!G || !out)) return SP24_ERR_INVALID_ARG;
+  if (!empty && (!aligned_to(G, 4) || !aligned_to(out, 2))) return SP24_ERR_MISALIGNED;
+  if ((st = check_device()) != SP24_OK) return st;
+  if (empty) return SP24_OK;
+  OrthSrc src = {};
+  src.g = G;
+  src.rows = rows;
+  src.cols = cols;
+  src.ld = ldg;
+  src.stride = batch_stride;
+  OrthOut o = {};
+  o.out16 = static_cast<uint16_t *>(out);
+  o.bf16 = dtype == SP24_BF16;
+  return run_orth(pl, src, o, steps, eps, workspace, as_stream(stream));
+}
+
+sp24_status sp24_muon_step(const float *grad, float *momentum, float *W, void *W16, sp24_dtype dtype, int64_t count,
+                           int64_t rows, int64_t cols, float mu, int nesterov, float lr, float weight_decay, float scale,
+                           int steps, float eps, void *workspace, size_t workspace_bytes, void *stream) {
+  OrthPlan pl;
+  sp24_status st = orth_plan(count, rows, cols, &pl);
+  if (st != SP24_OK) return st;
+  if (!valid_dtype(dtype)) return SP24_ERR_UNSUPPORTED_DTYPE;
+  if ((st = validate_orth(pl, steps, eps, workspace, workspace_bytes)) != SP24_OK) return st;
+  const bool empty = count == 0 || pl.m == 0;
+  if (!empty && (!grad || !momentum || !W)) return SP24_ERR_INVALID_ARG;
+  if (!empty && (!aligned_to(grad, 4) || !aligned_to(momentum, 4) || !aligned_to(W, 4) || !aligned_to(W16, 2)))
+    return SP24_ERR_MISALIGNED;
+  if ((st = check_device()) != SP24_OK) return st;
+  if (empty) return SP24_OK;
+  OrthSrc src = {};
+  src.g = grad;
+  src.m = momentum;
+  src.rows = rows;
+  src.cols = cols;
+  src.ld = cols;
+  src.stride = rows * cols;
+  src.mu = mu;
+  src.nesterov = nesterov ? 1 : 0;
+  OrthOut o = {};
+  o.out16 = static_cast<uint16_t *>(W16);
+  o.w = W;
+  o.keep = (float)(1.0 - (double)lr * (double)weight_decay);
+  o.step = (float)((double)lr * (double)scale);
+  o.bf16 = dtype == SP24_BF16;
+  return run_orth(pl, src, o, steps, eps, workspace, as_stream(stream));
+}
+
+sp24_status sp24_quantize_rows(const void *X, sp24_dtype dtype, int64_t rows, int64_t cols, int64_t ldx,
+                               const uint8_t *idx, int8_t *q, float *scale, void *stream) {
+  if (rows < 0 || cols < 0 || ldx < cols) return SP24_ERR_INVALID_ARG;
+  if (!valid_dtype(dtype)) return SP24_ERR_UNSUPPORTED_DTYPE;
+  if (idx && (rows % 4 || cols % 4)) return SP24_ERR_UNSUPPORTED_SHAPE;
+  if (rows > 0 && (!scale || (cols > 0 && (!X || !q)))) return SP24_ERR_INVALID_ARG;
+  if (rows > 0 && cols > 0 && (!aligned16(X) || !aligned16(q))) return SP24_ERR_MISALIGNED;
+  sp24_status st = check_device();
+  if (st != SP24_OK) return st;
+  if (rows == 0) return SP24_OK;
+  const uint16_t *x = static_cast<const uint16_t *>(X);
+  return dtype == SP24_BF16 ? launch_quant<true>(x, rows, cols, ldx, idx, q, scale, as_stream(stream))
+                            : launch_quant<false>(x, rows, cols, ldx, idx, q, scale, as_stream(stream));
+}
+
+sp24_status sp24_gemm_i8(const int8_t *Xq, const float *sx, int64_t T, int64_t K, const int8_t *Wq, const float *sw,
+                         int64_t N, sp24_dtype dtype, void *Y, sp24_epilogue epi, void *stream) {
+  if (T < 0 || K <= 0 || N <= 0) return SP24_ERR_INVALID_ARG;
+  if (!Wq || !sw || (T > 0 && (!Xq || !sx || !Y))) return SP24_ERR_INVALID_ARG;
+  if (!valid_dtype(dtype)) return SP24_ERR_UNSUPPORTED_DTYPE;
+  if (epi != SP24_EPI_NONE && epi != SP24_EPI_GELU) return SP24_ERR_INVALID_ARG;
+  if (K % 16 || N % 16 || K > kMaxI8K || T > INT32_MAX - 256 || N > INT32_MAX - 256) return SP24_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(Xq) || !aligned16(Wq) || !aligned16(Y)) return SP24_ERR_MISALIGNED;
+  sp24_status st = check_device();
+  if (st != SP24_OK) return st;
+  if (T == 0) return SP24_OK;
+  cudaStream_t s = as_stream(stream);
+  if (dtype == SP24_BF16)
+    return epi == SP24_EPI_GELU ? launch_i8<true, true>(Xq, T, K, Wq, N, Y, sx, sw, s)
+                                : launch_i8<true, false>(Xq, T, K, Wq, N, Y, sx, sw, s);
+  return epi == SP24_EPI_GELU ? launch_i8<false, true>(Xq, T, K, Wq, N, Y, sx, sw, s)
+                              : launch_i8<false, false>(Xq, T, K, Wq, N, Y, sx, sw, s);
 }
 
 sp24_status sp24_aux_packed_size(int64_t T, int64_t M, size_t *bytes) {
