@@ -453,18 +453,29 @@ def sp24_flip_rate(idx_prev, idx_cur, count, stream=None):
 
 def _one_device(*ts):
     """The CUDA device that all of `ts` (None allowed) live on."""
-    _need_device(*ts)
-    devices = {t.device for t in ts if t is not None}
-    if len(devices) != 1:
-        raise ValueError(f"sp24 takes tensors of one device, got {sorted(map(str, devices))}")
-    return devices.pop()
+    device = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("sp24 kernels take CUDA tensors only")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"sp24 takes tensors of one device, got {device} and {t.device}")
+    return device
 
 
 def _call_on(device, fn: str, stream, *args):
     """Calls the entry point with `device` current, on `stream` or that device's current stream."""
     import torch
-    with torch.cuda.device(device):
-        _check(fn, getattr(_lib, fn)(*args, _stream(stream)))
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _call_on(device, fn, stream, *args)
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    status = getattr(_lib, fn)(*args, s.cuda_stream)
+    if status != 0:
+        raise Sp24Error(fn, status)
 
 
 def _stack3(t, name: str):

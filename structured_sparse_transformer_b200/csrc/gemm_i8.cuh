@@ -1,0 +1,245 @@
+// 8-bit forward product on CTA pairs (tcgen05 kind::i8, cta_group::2, sm_100a):
+//   Y[T x N] = (Xq Wq^T) sw sx, optionally gelu of it.
+//
+// A = Wq (feature = tensor-memory lane), B = Xq (token = accumulator column), both K-major in
+// rows of 128 bytes; exact 32-bit integer accumulation, then (float(acc) * sw[n]) * sx[t] in
+// fp32 and one rounding to the dtype.  A pair computes 256 features x BN tokens; each CTA
+// holds 128 rows of Wq and BN/2 rows of Xq per 128-deep stage, the pair's even CTA issues the
+// MMAs (K = 32 each).  Persistent over tiles, features fastest (the pairs running at once
+// share token tiles through L2), two accumulators, so a tile's epilogue overlaps the next
+// tile's main loop.
+//
+// Warps: 0 = TMA producer, 1 = TMEM allocation and (leader) MMA issue, 2-17 = epilogue, four
+// groups of four warps on alternate 32-token chunks: registers -> 16-bit pairs ->
+// stmatrix.trans into a staging tile [32 tokens x 32 features] -> one TMA store.  Every wait
+// is bounded.
+#pragma once
+#include "gemm_sp.cuh"
+
+namespace sp24 {
+
+constexpr int kI8EpiWarps = 16;
+constexpr int kI8Threads = 64 + 32 * kI8EpiWarps;
+constexpr int kI8BarBytes = 512;
+constexpr int kI8TileBytes = 32 * 32 * 2;              // staging tile, 64B-swizzled
+
+template <int BN>
+struct I8Geom {
+  static constexpr int kSmemA = 128 * 128;
+  static constexpr int kSmemB = (BN / 2) * 128;
+  static constexpr int kStageBytes = kSmemA + kSmemB;
+  static constexpr int kFixed = 1024 + kI8BarBytes + kI8EpiWarps * kI8TileBytes;
+  static constexpr int kStages = (232448 - kFixed) / kStageBytes < 8 ? (232448 - kFixed) / kStageBytes : 8;
+  static constexpr int kSmem = kStages * kStageBytes + kFixed;
+  static constexpr int kChunks = BN / 32;
+  static_assert(BN == 128 || BN == 256, "tile widths");
+  static_assert(kStages >= 4 && 8 * (2 * kStages + 6) <= kI8BarBytes, "shared memory per CTA");
+  static_assert(kStageBytes % 1024 == 0, "128B-swizzled tiles need 1 KB aligned starts");
+};
+
+template <int BN, bool BF16, bool GELU>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
+    gemm_i8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                   const __grid_constant__ CUtensorMap tm_y, int N, int T, int num_kt, uint64_t wait_budget,
+                   const float *__restrict__ sw, const float *__restrict__ sx) {
+  using G = I8Geom<BN>;
+  constexpr int kStages = G::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *epi_smem = smem + kStages * G::kStageBytes;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(epi_smem + kI8EpiWarps * kI8TileBytes);
+  uint64_t *full = bars;                       // [stages] leader: TMA (both CTAs) -> MMA
+  uint64_t *empty = bars + kStages;            // [stages] MMA -> this CTA's TMA
+  uint64_t *acc_full = bars + 2 * kStages;     // [2] MMA -> this CTA's epilogue
+  uint64_t *acc_empty = acc_full + 2;          // [2] leader: both epilogues -> MMA
+  uint64_t *drain = acc_empty + 2;
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(drain + 1);
+  volatile int *s_abort = reinterpret_cast<volatile int *>(s_tmem + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool is_leader = rank == 0;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int num_mt = (N + 255) / 256;
+  const int num_tiles = num_mt * ((T + BN - 1) / BN);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 2 * kI8EpiWarps);
+    }
+    mbar_init(drain, 1);
+    *s_abort = 0;
+    fence_mbarrier_init();
+    prefetch_tensormap(&tm_w);
+    prefetch_tensormap(&tm_x);
+    prefetch_tensormap(&tm_y);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(s_tmem, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before any cross-CTA arrive or byte count
+  tc_fence_after();
+  const uint32_t tmem_base = *s_tmem;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------ producer (both CTAs)
+    uint32_t g = 0;
+    bool ok = true;
+    for (int tile = pair; ok && tile < num_tiles; tile += npairs) {
+      const int w_row = (tile % num_mt) * 256 + (int)rank * 128, x_row = (tile / num_mt) * BN + (int)rank * (BN / 2);
+      for (int kt = 0; kt < num_kt; ++kt, ++g) {
+        const int s = (int)(g % kStages);
+        if (!mbar_wait_bounded(&empty[s], ((g / kStages) & 1u) ^ 1u, wait_budget, s_abort)) {
+          ok = false;
+          break;
+        }
+        uint8_t *st = smem + s * G::kStageBytes;
+        if (is_leader) mbar_arrive_expect_tx(&full[s], 2 * G::kStageBytes);
+        tma_load_2d_pair(st, &tm_w, &full[s], kt * 128, w_row);
+        tma_load_2d_pair(st + G::kSmemA, &tm_x, &full[s], kt * 128, x_row);
+      }
+    }
+    // The leader's `full` barriers count both CTAs' bytes: let every copy land.
+    if (is_leader) {
+      for (uint32_t i = g > kStages ? g - kStages : 0; i < g; ++i) {
+        volatile int no_abort = 0;
+        mbar_wait_bounded(&full[i % kStages], (i / kStages) & 1u, kDrainBudget, &no_abort);
+      }
+    }
+  } else if (warp == 1 && lane == 0 && is_leader) {
+    // ----------------------------------------------------- MMA issuer (leader)
+    constexpr uint32_t idesc = make_idesc_i8(256, BN);
+    const uint64_t a_desc0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+    const uint64_t b_desc0 = smem_desc(smem_u32(smem + G::kSmemA), 16, 1024, kSwizzle128B);
+    uint32_t g = 0;
+    bool ok = true;
+    int j = 0;
+    for (int tile = pair; ok && tile < num_tiles; tile += npairs, ++j) {
+      const int buf = j & 1;
+      if (!(ok = mbar_wait_bounded(&acc_empty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, wait_budget, s_abort))) break;
+      tc_fence_after();
+      const uint32_t acc = tmem_base + (uint32_t)(buf * BN);
+      for (int kt = 0; kt < num_kt; ++kt, ++g) {
+        const int s = (int)(g % kStages);
+        if (!(ok = mbar_wait_bounded(&full[s], (g / kStages) & 1u, wait_budget, s_abort))) break;
+        tc_fence_after();
+        const uint64_t so = (uint64_t)((s * G::kStageBytes) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)   // 32 bytes along the 128-byte swizzled rows each
+          tc_mma_i8_pair(acc, a_desc0 + so + 2 * kk, b_desc0 + so + 2 * kk, idesc, (kt != 0 || kk != 0) ? 1u : 0u);
+        tc_commit_pair(&empty[s], 0x3);
+      }
+      if (ok) tc_commit_pair(&acc_full[buf], 0x3);
+    }
+    if (!ok) {
+      tc_commit_pair(drain, 0x1);
+      volatile int no_abort = 0;
+      mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
+    }
+  } else if (warp >= 2) {
+    // ---------------------------------------------------- epilogue (both CTAs)
+    // Warp w drains lanes 32q..32q+31 (q = w%4) at the 32-token chunks grp, grp + 4.  Register
+    // 4i + 2 sub + e of block [h][g], lane l: feature 16h + 8 sub + l/4, token 16g + 8i +
+    // 2(l%4) + e of the chunk.
+    const int ew = warp - 2, grp = ew >> 2, q = warp & 3;
+    uint8_t *stg = epi_smem + ew * kI8TileBytes;
+    const uint32_t stg_u32 = smem_u32(stg);
+    const int lr = lane >> 2, lc = 2 * (lane & 3);
+    bool alive = true;
+    int j = 0;
+    for (int tile = pair; alive && tile < num_tiles; tile += npairs, ++j) {
+      const int m0 = (tile % num_mt) * 256 + (int)rank * 128 + 32 * q, n0 = (tile / num_mt) * BN;
+      const int nch = min(G::kChunks, (T - n0 + 31) / 32);
+      float fw[4];   // [2h + sub]
+#pragma unroll
+      for (int e = 0; e < 4; ++e) fw[e] = m0 + 8 * e + lr < N ? __ldg(sw + m0 + 8 * e + lr) : 0.0f;
+      float2 fx[2][2];   // the first chunk's token scales, [g][i]
+      auto load_sx = [&](int c0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = c0 + 8 * e + lc;
+          fx[e >> 1][e & 1] = make_float2(t < T ? __ldg(sx + t) : 0.0f, t + 1 < T ? __ldg(sx + t + 1) : 0.0f);
+        }
+      };
+      load_sx(n0 + 32 * grp);
+      const int buf = j & 1;
+      const bool got = mbar_wait_bounded(&acc_full[buf], (uint32_t)(j >> 1) & 1u, wait_budget, s_abort);
+      if (!__all_sync(0xFFFFFFFFu, got)) {
+        alive = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t t_base = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * BN);
+      constexpr int kPerWarp = (G::kChunks + 3) / 4;
+#pragma unroll
+      for (int k = 0; k < kPerWarp; ++k) {
+        const int ch = grp + 4 * k;
+        uint32_t r[2][2][8];
+        if (ch < nch) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+              tmem_ld_16x256b_x2(t_base + ((uint32_t)(16 * h) << 16) + (uint32_t)(32 * ch + 16 * g), r[h][g]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int hg = 0; hg < 4; ++hg) reg_fence(r[hg >> 1][hg & 1]);
+        }
+        if (k == kPerWarp - 1) {   // the accumulator goes back to the MMA
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_leader(&acc_empty[buf]);
+        }
+        if (ch >= nch) continue;
+        const int c0 = n0 + 32 * ch;
+        if (k > 0) load_sx(c0);
+        uint32_t pk[2][2][4];   // [h][g][2i + sub]
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float s = fw[2 * h + (e & 1)];
+              const float2 x = fx[g][e >> 1];
+              float2 v = make_float2((__int2float_rn((int)r[h][g][2 * e]) * s) * x.x,
+                                     (__int2float_rn((int)r[h][g][2 * e + 1]) * s) * x.y);
+              if (GELU) v = gelu2(v);
+              pk[h][g][e] = pack2<BF16>(v.x, v.y);
+            }
+        if (lane == 0) bulk_wait_group_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+            stmatrix_x4_trans(stg_u32 + swz64(16 * g + 8 * (lane >> 4) + (lane & 7), 2 * h + ((lane >> 3) & 1)), pk[h][g]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && m0 < N) {   // the TMA unit clips features and tokens past the matrix
+          tma_store_2d(&tm_y, stg, m0, c0);
+          bulk_commit_group();
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_group<0>();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the peer's MMAs, copies and arrivals into this CTA are over
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+}  // namespace sp24

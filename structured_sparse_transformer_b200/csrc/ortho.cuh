@@ -1,4 +1,4 @@
-// Passes of the optimiser step around the Newton-Schulz products (gemm_nt.cuh): the
+// Passes of the optimiser step around the Newton-Schulz products (ortho_gemm.cuh): the
 // momentum update with the sum of squares, and the scaling of the update direction to the
 // fp16 iterate X0 = s U / (|U|_F + eps), transposed when the matrix is tall, so that the
 // products always work on its short side.
@@ -13,7 +13,7 @@ namespace sp24 {
 
 constexpr int kOrthThreads = 256;
 constexpr int kOrthMaxBlocks = 512;    // partial sums per matrix
-constexpr int kOrthTile = 64;          // transposing pass: 64 x 64 entries per block
+constexpr int kOrthTile = 64;          // tile of the scaling pass
 
 struct OrthSrc {
   const float *g;            // gradient (Orth: the matrix itself)
@@ -96,41 +96,80 @@ __device__ __forceinline__ float2 orth_factor(double sumsq, float s, float eps) 
   return make_float2((float)f1, (float)(f / f1));
 }
 
-// Grid (column tiles, row tiles, matrices) of 64 x 64 entries.  x [matrices][short][ldx] fp16.
-template <bool TALL>
+// Grid (blocks, matrices); a block takes every gridDim.x-th 64 x 64 tile of its matrix.  x is
+// [matrices][short][ldx] fp16.  QUADS: rows of whole aligned float4s.  A tall matrix is
+// transposed through shared memory (rows of 33 words, so that the column reads spread over
+// the banks); stores of four entries may run into the padding of a row of x, never past it.
+template <bool TALL, bool QUADS>
 __global__ void __launch_bounds__(kOrthThreads)
     orth_scale_kernel(const OrthSrc p, const double *__restrict__ part, int nparts, float s, float eps,
-                      __half *__restrict__ x, int64_t ldx, int64_t row_tiles) {
-  __shared__ __half s_t[kOrthTile][kOrthTile + 2];
+                      __half *__restrict__ x, int64_t ldx, int64_t col_tiles, int64_t tiles,
+                      unsigned *__restrict__ counters, int ncounters) {
+  __shared__ __align__(16) __half s_t[kOrthTile][kOrthTile + 2];
+  __shared__ float2 s_f;
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t b = blockIdx.z;
+  if (blockIdx.x == 0 && blockIdx.y == 0)   // the products' counters (ortho_gemm.cuh)
+    for (int i = threadIdx.x; i < ncounters; i += kOrthThreads) counters[i] = 0u;
+  const int64_t b = blockIdx.y;
   double t = 0.0;
   for (int i = threadIdx.x; i < nparts; i += kOrthThreads) t += part[b * nparts + i];
-  const float2 f = orth_factor(block_sum(t), s, eps);
+  t = block_sum(t);
+  if (threadIdx.x == 0) s_f = orth_factor(t, s, eps);
+  __syncthreads();
+  const float2 f = s_f;
   const float *g = p.g + b * p.stride;
   const float *m = p.m ? p.m + b * p.stride : nullptr;
-  const int64_t c0 = (int64_t)blockIdx.x * kOrthTile;
-  const int tc = threadIdx.x & 63, tr = threadIdx.x >> 6;
-  for (int64_t rt = blockIdx.y; rt < row_tiles; rt += gridDim.y) {
-    const int64_t r0 = rt * kOrthTile;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  // From the end of the matrix: what the pass before touched last is what the cache still holds.
+  for (int64_t tile = tiles - 1 - blockIdx.x; tile >= 0; tile -= gridDim.x) {
+    const int64_t r0 = tile / col_tiles * kOrthTile, c0 = tile % col_tiles * kOrthTile;
+    float4 gv[4], mv[4];
 #pragma unroll
-    for (int k = 0; k < kOrthTile / 4; ++k) {
-      const int64_t r = r0 + tr + 4 * k, c = c0 + tc;
-      if (r < p.rows && c < p.cols) {
-        const float gv = g[r * p.ld + c];
-        const float u = m ? orth_dir(p, gv, m[r * p.ld + c]) : gv;
-        const __half h = __float2half_rn(u * f.x * f.y);
-        if (TALL) s_t[tr + 4 * k][tc] = h;
-        else x[(b * p.rows + r) * ldx + c] = h;
+    for (int k = 0; k < 4; ++k) {
+      const int64_t r = r0 + ty + 16 * k, c = c0 + 4 * tx;
+      float *ge = reinterpret_cast<float *>(&gv[k]), *me = reinterpret_cast<float *>(&mv[k]);
+      gv[k] = mv[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r >= p.rows) continue;
+      if (QUADS) {
+        if (c < p.cols) {
+          gv[k] = *reinterpret_cast<const float4 *>(g + r * p.ld + c);
+          if (m) mv[k] = *reinterpret_cast<const float4 *>(m + r * p.ld + c);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < p.cols) {
+            ge[e] = g[r * p.ld + c + e];
+            if (m) me[e] = m[r * p.ld + c + e];
+          }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float *ge = reinterpret_cast<const float *>(&gv[k]), *me = reinterpret_cast<const float *>(&mv[k]);
+      __align__(8) __half h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = __float2half_rn((m ? orth_dir(p, ge[e], me[e]) : ge[e]) * f.x * f.y);
+      const int64_t r = r0 + ty + 16 * k, c = c0 + 4 * tx;
+      if (TALL) {
+        *reinterpret_cast<__half2 *>(&s_t[ty + 16 * k][4 * tx]) = __halves2half2(h[0], h[1]);
+        *reinterpret_cast<__half2 *>(&s_t[ty + 16 * k][4 * tx + 2]) = __halves2half2(h[2], h[3]);
+      } else if (r < p.rows && c < p.cols) {
+        *reinterpret_cast<uint2 *>(x + (b * p.rows + r) * ldx + c) = *reinterpret_cast<const uint2 *>(h);
       }
     }
     if (TALL) {
       __syncthreads();
 #pragma unroll
-      for (int k = 0; k < kOrthTile / 4; ++k) {
-        const int64_t c = c0 + tr + 4 * k, r = r0 + tc;
-        if (r < p.rows && c < p.cols) x[(b * p.cols + c) * ldx + r] = s_t[tc][tr + 4 * k];
+      for (int k = 0; k < 4; ++k) {
+        const int cc = ty + 16 * k;
+        const int64_t c = c0 + cc, r = r0 + 4 * tx;
+        __align__(8) __half h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = s_t[4 * tx + e][cc];
+        if (c < p.cols && r < p.rows)
+          *reinterpret_cast<uint2 *>(x + (b * p.cols + c) * ldx + r) = *reinterpret_cast<const uint2 *>(h);
       }
       __syncthreads();
     }

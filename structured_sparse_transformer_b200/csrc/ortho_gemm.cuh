@@ -1,0 +1,824 @@
+// The Newton-Schulz products of the orthogonalisation (sm_100a).
+//
+// Per round, on the short side m of a stack of matrices X [m x n]:
+//   Gram    G = X X^T / s^2            (X = s times the iterate)
+//   Poly    P = a I + b G + c G^2      (G symmetric, so G^2 = G G^T)
+//   Apply   X <- P X
+// The last round's product with X goes to its destination in a kernel of its own
+// (orth_last_kernel): the 16-bit result, or the weight, W <- keep W - step (P X), W16 <- W.
+//
+// orth_products_kernel is one cooperative launch of CTA pairs (tcgen05 cta_group::2, 256 x 256
+// tiles, fp16 operands, fp32 accumulation) that runs all other phases one after another.  A
+// phase needs everything the one before wrote, so at its end every epilogue warp counts up a
+// counter of the phase once its stores are complete, and every TMA producer waits for the
+// counts: only the producers stall, tensor memory, barriers and descriptors stay set up.
+// (As 15 launches, each phase paid for launch, set-up and drain: about 9 us each.)
+//
+// Gram and Poly are symmetric: only tiles on and below the diagonal are computed, and a tile
+// below it is stored a second time, transposed (stmatrix.trans on the same registers), so
+// they cost half of the full product.  Where a phase has fewer tiles than pairs, or a last
+// wave does, its tiles are split along K (PairSchedule).  Each part then finishes its share of
+// the tile's 32-column chunks: it passes the others' chunks on as fp32 partial sums and adds
+// what they passed for its own, in part order (every part writes and reads (s-1)/s of a tile,
+// where one part adding all of them would wait for s-1 whole tiles).
+//
+// orth_last_kernel's tensor-memory lanes are the matrix's columns, so that a warp's 32 lanes
+// touch 32 neighbouring entries of a row whatever its alignment: a tall matrix takes P X as
+// it is (X holds its transpose), a wide one (P X)^T = X^T P with X as the MN-major A operand.
+//
+// Fewer bits: the iterate, G and P are held in fp16.  With X scaled by a power of two s near
+// sqrt(n), its entries are of the order of one whatever the size of the matrix and at most 2 s,
+// so fp16 neither overflows nor loses small entries, and its 11-bit significand leaves about
+// 1e-3 of relative error after five rounds, where bf16 (8 bits) leaves about 9e-3.  Folding
+// a I into P (instead of adding a X in the epilogue) spares the epilogue a read of X and
+// leaves the same error.
+//
+// Warps: 0 = TMA producer, 1 = TMEM allocation and (leader) MMA issue, 2-9 = epilogue, two
+// groups of four warps on one half of the columns each.  A phase's tail is its last tiles'
+// epilogues, so a warp takes half of its 32 x 128 block through every step at once (tensor
+// memory -> registers -> fp16 pairs -> stmatrix -> TMA store): chunk by chunk, each step's
+// latency is paid four times (3.6 us a tile).  Every wait is bounded.
+#pragma once
+#include "gemm_sp.cuh"
+
+namespace sp24 {
+
+enum : int { kOrthGram = 0, kOrthPoly = 1, kOrthApply = 2 };
+
+constexpr int kOgTileBytes = 32 * 32 * 2;              // staging tile: 32 x 32 16-bit values, 64B-swizzled
+constexpr int kOgBarBytes = 512;
+constexpr int kOgEpiWarps = 8;
+constexpr int kOgThreads = 64 + 32 * kOgEpiWarps;
+constexpr int kOgStageBytes = 2 * 128 * 128;           // A 128 rows and B 128 rows (or two atoms) of 128 bytes
+constexpr int kOgChunks = 4;                           // 32-column chunks of a warp: 128 of the tile's 256 columns
+constexpr int kOgStagingBytes = kOgChunks * kOgTileBytes;   // per epilogue warp
+constexpr int kOgStages = 5;
+constexpr int kOgSmem = kOgStages * kOgStageBytes + kOgEpiWarps * kOgStagingBytes + kOgBarBytes + 1024;
+constexpr int kOgMaxSplit = 4;                         // parts of a split tile: a warp has four chunks to share
+constexpr int kOgMaxPairs = 80;
+constexpr int kOgMaxSteps = 16;
+// Partial sums of one CTA of a split tile: per epilogue warp and chunk, the registers of its
+// tensor-memory load as eight float4 per lane.
+constexpr int64_t kOgPartFloats = (int64_t)kOgEpiWarps * kOgChunks * 8 * 32 * 4;
+// Counters at the front of the workspace, zero at launch: per epilogue warp and phase, the CTAs
+// whose warp has finished it (one counter per warp, so that each warp releases its own stores
+// and no address takes more than one increment per CTA); then per (CTA, epilogue warp), 1 +
+// the last phase whose partial sums it has passed on.
+constexpr int kOgPhases = 64;
+constexpr int kOgPhaseCounters = kOgPhases * kOgEpiWarps;
+constexpr int kOgCounters = kOgPhaseCounters + 2 * kOgMaxPairs * kOgEpiWarps;
+static_assert(3 * kOgMaxSteps <= kOgPhases, "a counter per phase");
+static_assert(kOgSmem <= 232448 && 8 * (2 * kOgStages + 7 + kOgEpiWarps) <= kOgBarBytes,
+              "shared memory per CTA");
+
+struct OrthMaps {
+  CUtensorMap x_rows[2], x_cols[2], x_st[2], g_rows, g_st, p_rows, p_st;
+};
+
+struct OrthProducts {
+  int m, n;                  // short and long side
+  int batch, phases;
+  int sym_tiles, tiles;      // tiles of the symmetric products and of P X, per matrix
+  int split[3];              // parts of a tail tile, by kind
+  uint64_t wait_budget;
+  float gram_alpha;          // 1 / s^2
+  float a, b, c;
+  float *part;
+  unsigned *counters;
+};
+
+struct OrthPhase {
+  int kind, in, num_kt, tiles, split;
+  __device__ OrthPhase(const OrthProducts &p, int ph) {
+    kind = ph % 3;
+    in = (ph / 3) & 1;
+    num_kt = ((kind == kOrthGram ? p.n : p.m) + 63) >> 6;
+    tiles = p.batch * (kind == kOrthApply ? p.tiles : p.sym_tiles);
+    split = p.split[kind];
+  }
+};
+
+// Matrix, first row and first column of a tile; `below`: strictly below the diagonal.
+__device__ __forceinline__ void orth_tile(const OrthProducts &p, int kind, int t, int &b, int &m0, int &n0, bool &below) {
+  if (kind != kOrthApply) {   // row block i has column blocks 0..i
+    b = t / p.sym_tiles;
+    t -= b * p.sym_tiles;
+    int i = (int)((sqrtf(1.0f + 8.0f * (float)t) - 1.0f) * 0.5f);
+    while (i * (i + 1) / 2 > t) --i;
+    while ((i + 1) * (i + 2) / 2 <= t) ++i;
+    const int j = t - i * (i + 1) / 2;
+    m0 = i * 256;
+    n0 = j * 256;
+    below = j < i;
+  } else {
+    b = t / p.tiles;
+    t -= b * p.tiles;
+    const int num_mt = (p.m + 255) / 256;
+    m0 = (t % num_mt) * 256;
+    n0 = (t / num_mt) * 256;
+    below = false;
+  }
+}
+
+// Four 8x8 16-bit matrices, as held (no transpose): register j of thread t is row t/4,
+// columns 2(t%4) and 2(t%4)+1 of matrix j; lane 8j + r gives the address of its row r.
+__device__ __forceinline__ void stmatrix_x4(uint32_t saddr, const uint32_t (&r)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
+// The reverse of stmatrix_x4.
+__device__ __forceinline__ void ldmatrix_x4(uint32_t saddr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(saddr)
+               : "memory");
+}
+
+// 16 tensor-memory lanes x 32 columns: tmem_ld_16x256b_x2's layout over four 8-column blocks.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// TMA tile load into this CTA's shared memory, counted on its own mbarrier.
+__device__ __forceinline__ void tma_load_3d(void *smem_dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Wait until *flag >= target without sleeping (the phase's start waits on it).
+__device__ __forceinline__ bool flag_spin_bounded(const unsigned *flag, unsigned target, uint64_t budget,
+                                                  volatile int *abort_flag) {
+  if (flag_load_acquire(flag) >= target) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (*abort_flag) return false;
+    if ((uint64_t)(clock64() - t0) > budget) {
+      *abort_flag = 1;
+      record_device_error(kDevErrTimeout);
+      return false;
+    }
+    if (flag_load_acquire(flag) >= target) return true;
+  }
+}
+
+__device__ __forceinline__ void flag_store_release(unsigned *flag, unsigned v) {
+  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(flag), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// Uses of the loaded registers stay below the wait.
+__device__ __forceinline__ void regs_fence(uint32_t (&r)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// Passes on a warp's chunks that other parts finish.  Not inlined: inlined, the compiler keeps
+// its registers beside the epilogue's and spills.
+__device__ __noinline__ void orth_pass_chunks(uint32_t taddr, int nch, int part, int parts, float4 *slot) {
+#pragma unroll 1
+  for (int kk = 0; kk < nch; ++kk) {
+    if (((kk * parts) >> 2) == part) continue;
+    uint32_t r[2][16];
+    tmem_ld_16x256b_x4(taddr + (uint32_t)(32 * kk), r[0]);
+    tmem_ld_16x256b_x4(taddr + (uint32_t)(32 * kk) + (16u << 16), r[1]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      regs_fence(r[h]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        __stcg(slot + (kk * 8 + 4 * h + e) * 32,
+               make_float4(__uint_as_float(r[h][4 * e]), __uint_as_float(r[h][4 * e + 1]),
+                           __uint_as_float(r[h][4 * e + 2]), __uint_as_float(r[h][4 * e + 3])));
+    }
+  }
+}
+
+// Two 32-column chunks (the first n of them) as the fragments of 16x256b: [chunk][h].
+__device__ __forceinline__ void orth_load_half(uint32_t taddr, int n, uint32_t (&r)[2][2][16]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (k < n) {
+      tmem_ld_16x256b_x4(taddr + (uint32_t)(32 * k), r[k][0]);
+      tmem_ld_16x256b_x4(taddr + (uint32_t)(32 * k) + (16u << 16), r[k][1]);
+    }
+  tmem_wait_ld();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) regs_fence(r[k >> 1][k & 1]);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
+    orth_products_kernel(const __grid_constant__ OrthMaps maps, const __grid_constant__ OrthProducts p) {
+  constexpr int kStages = kOgStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *epi_smem = smem + kStages * kOgStageBytes;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(epi_smem + kOgEpiWarps * kOgStagingBytes);
+  uint64_t *full = bars;                       // [stages] leader: TMA (both CTAs) -> MMA
+  uint64_t *empty = bars + kStages;            // [stages] MMA -> this CTA's TMA
+  uint64_t *acc_full = bars + 2 * kStages;     // [2] MMA -> this CTA's epilogue
+  uint64_t *acc_empty = acc_full + 2;          // [2] leader: both epilogues -> MMA
+  uint64_t *drain = acc_empty + 2;
+  uint64_t *ready = drain + 1;                 // producer -> epilogue: the phase's inputs are written
+  uint64_t *g_bars = ready + 1;                // [epilogue warps] G's entries of a Poly tile
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(g_bars + kOgEpiWarps);
+  volatile int *s_abort = reinterpret_cast<volatile int *>(s_tmem + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool is_leader = rank == 0;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 2 * kOgEpiWarps);
+    }
+    mbar_init(drain, 1);
+    mbar_init(ready, 1);
+    for (int w = 0; w < kOgEpiWarps; ++w) mbar_init(&g_bars[w], 1);
+    *s_abort = 0;
+    fence_mbarrier_init();
+    prefetch_tensormap(&maps.x_rows[0]);
+    prefetch_tensormap(&maps.g_rows);
+    prefetch_tensormap(&maps.g_st);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(s_tmem, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before any cross-CTA arrive or byte count
+  tc_fence_after();
+  const uint32_t tmem_base = *s_tmem;
+
+  if (warp == 0) {
+    // ------------------------------------------------------ producer (both CTAs)
+    // Lane w waits for the epilogue warps w of every CTA; lane 0 issues the loads.
+    uint32_t g = 0;
+    bool ok = true;
+    for (int ph = 0; ok && ph < p.phases; ++ph) {
+      bool up = true;
+      if (ph > 0 && lane < kOgEpiWarps)   // all of the phase before is written
+        up = flag_spin_bounded(p.counters + lane * kOgPhases + ph - 1, gridDim.x, p.wait_budget, s_abort);
+      if (!__all_sync(0xFFFFFFFFu, up)) break;
+      __syncwarp();
+      if (lane == 0) {
+        const OrthPhase f(p, ph);
+        const CUtensorMap *ma, *mb;
+        const bool b_mn = f.kind == kOrthApply;
+        if (f.kind == kOrthGram) {
+          ma = mb = &maps.x_rows[f.in];
+        } else if (f.kind == kOrthPoly) {
+          ma = mb = &maps.g_rows;
+        } else {
+          ma = &maps.p_rows;
+          mb = &maps.x_cols[f.in];
+        }
+        prefetch_tensormap(ma);
+        prefetch_tensormap(mb);
+        fence_proxy_async_all();
+        mbar_arrive(ready);
+        PairSchedule sched(f.split, pair, npairs, f.tiles, f.num_kt);
+        int tile, kb, ke;
+        while (ok && sched.next(tile, kb, ke)) {
+          int b, m0, n0;
+          bool below;
+          orth_tile(p, f.kind, tile, b, m0, n0, below);
+          const int a_row = m0 + (int)rank * 128, b_row = n0 + (int)rank * 128;
+          for (int kt = kb; kt < ke; ++kt, ++g) {
+            const int s = (int)(g % kStages);
+            if (!mbar_wait_bounded(&empty[s], ((g / kStages) & 1u) ^ 1u, p.wait_budget, s_abort)) {
+              ok = false;
+              break;
+            }
+            uint8_t *st = smem + s * kOgStageBytes;
+            if (is_leader) mbar_arrive_expect_tx(&full[s], 2 * kOgStageBytes);
+            // K-major: 128 rows of 64 entries along K; MN-major: two 64-column atoms of 64 rows.
+            tma_load_3d_pair(st, ma, &full[s], kt * 64, a_row, b);
+            if (b_mn) {
+              tma_load_3d_pair(st + 16384, mb, &full[s], b_row, kt * 64, b);
+              tma_load_3d_pair(st + 24576, mb, &full[s], b_row + 64, kt * 64, b);
+            } else {
+              tma_load_3d_pair(st + 16384, mb, &full[s], kt * 64, b_row, b);
+            }
+          }
+        }
+      }
+      ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+    }
+    // The leader's `full` barriers count both CTAs' bytes: let every copy land.
+    if (is_leader && lane == 0) {
+      for (uint32_t i = g > kStages ? g - kStages : 0; i < g; ++i) {
+        volatile int no_abort = 0;
+        mbar_wait_bounded(&full[i % kStages], (i / kStages) & 1u, kDrainBudget, &no_abort);
+      }
+    }
+  } else if (warp == 1 && lane == 0 && is_leader) {
+    // ----------------------------------------------------- MMA issuer (leader)
+    uint32_t g = 0;
+    bool ok = true;
+    int j = 0;
+    for (int ph = 0; ok && ph < p.phases; ++ph) {
+      const OrthPhase f(p, ph);
+      const bool b_mn = f.kind == kOrthApply;
+      const uint32_t idesc = make_idesc_dense(false, 256, 256) | (b_mn ? 1u << 16 : 0u);
+      const uint64_t a_desc0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+      const uint64_t b_desc0 = smem_desc(smem_u32(smem + 16384), b_mn ? 8192 : 16, 1024, kSwizzle128B);
+      // A K step of 16 moves 32 bytes along the rows, or 16 rows of 128 bytes.
+      const uint64_t b_step = b_mn ? 2048 >> 4 : 2;
+      PairSchedule sched(f.split, pair, npairs, f.tiles, f.num_kt);
+      int tile, kb, ke;
+      for (; ok && sched.next(tile, kb, ke); ++j) {
+        const int buf = j & 1;
+        if (!(ok = mbar_wait_bounded(&acc_empty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, p.wait_budget, s_abort))) break;
+        tc_fence_after();
+        const uint32_t acc = tmem_base + (uint32_t)(buf * 256);
+        for (int kt = kb; kt < ke; ++kt, ++g) {
+          const int s = (int)(g % kStages);
+          if (!(ok = mbar_wait_bounded(&full[s], (g / kStages) & 1u, p.wait_budget, s_abort))) break;
+          tc_fence_after();
+          const uint64_t so = (uint64_t)((s * kOgStageBytes) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_f16_pair(acc, a_desc0 + so + 2 * kk, b_desc0 + so + kk * b_step, idesc,
+                            (kt != kb || kk != 0) ? 1u : 0u);
+          tc_commit_pair(&empty[s], 0x3);
+        }
+        if (ok) tc_commit_pair(&acc_full[buf], 0x3);
+      }
+    }
+    if (!ok) {
+      tc_commit_pair(drain, 0x1);
+      volatile int no_abort = 0;
+      mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
+    }
+  } else if (warp >= 2) {
+    // ---------------------------------------------------- epilogue (both CTAs)
+    // Warp w drains lanes 32q..32q+31 (q = w%4) at columns 128 grp .. 128 grp + 127, four chunks
+    // of 32.  Gram, Poly and Apply: register 16h + 4i + 2 sub + e of chunk kk, lane l, is row
+    // 16h + 8 sub + l/4, column 8i + 2(l%4) + e of the chunk.  Last: register i is column i
+    // of row l.
+    const int ew = warp - 2, grp = ew >> 2, q = warp & 3;
+    uint8_t *stg = epi_smem + ew * kOgStagingBytes;
+    const uint32_t stg_u32 = smem_u32(stg);
+    uint64_t *g_bar = &g_bars[ew];
+    uint32_t g_issued = 0, g_used = 0;   // Poly tiles' loads of G
+    const int lr = lane >> 2, lc = 2 * (lane & 3);
+    // stmatrix and ldmatrix of a 16 x 16 block: lane l names row l%8 of matrix l/8; matrix
+    // 2i + sub holds rows 8 sub.., columns 8i...
+    const int d_row = 8 * ((lane >> 3) & 1) + (lane & 7), d_unit = lane >> 4;
+    const int t_row = 8 * (lane >> 4) + (lane & 7), t_unit = (lane >> 3) & 1;
+    // Split tiles: this warp's slot and counter; those of the part d pairs on are 2 d CTAs further.
+    float4 *part_own = reinterpret_cast<float4 *>(p.part + (int64_t)blockIdx.x * kOgPartFloats) +
+                       (int64_t)ew * kOgChunks * 8 * 32 + lane;
+    unsigned *flag_own = p.counters + kOgPhaseCounters + (int64_t)blockIdx.x * kOgEpiWarps + ew;
+    bool alive = true;
+    int j = 0;
+    for (int ph = 0; alive && ph < p.phases; ++ph) {
+      const OrthPhase f(p, ph);
+      const CUtensorMap *mo = f.kind == kOrthGram ? &maps.g_st : (f.kind == kOrthPoly ? &maps.p_st : &maps.x_st[1 - f.in]);
+      const int N = f.kind == kOrthApply ? p.n : p.m;
+      if (lane == 0) prefetch_tensormap(mo);
+      PairSchedule sched(f.split, pair, npairs, f.tiles, f.num_kt);
+      int tile, kb, ke;
+      for (; alive && sched.next(tile, kb, ke); ++j) {
+        int b, m0, n0;
+        bool below;
+        orth_tile(p, f.kind, tile, b, m0, n0, below);
+        m0 += (int)rank * 128 + 32 * q;
+        n0 += 128 * grp;
+        const bool split = ke - kb < f.num_kt;
+        const int part = split ? pair % f.split : 0, parts = split ? f.split : 1;
+        const int nch = min(kOgChunks, (N - n0 + 31) >> 5);   // chunks inside the matrix (none: <= 0)
+        const int buf = j & 1;
+        auto mine = [&](int kk) { return kk < nch && ((kk * parts) >> 2) == part; };   // chunks that this part finishes
+        // The other parts have passed on this warp's chunks: one lane waits for each.
+        auto others_ready = [&]() {
+          bool ready_flag = true;
+          if (lane < parts && lane != part)
+            ready_flag = flag_spin_bounded(flag_own + 2 * (lane - part) * kOgEpiWarps, (unsigned)ph + 1, p.wait_budget, s_abort);
+          const bool all = __all_sync(0xFFFFFFFFu, ready_flag);
+          __syncwarp();
+          return all;
+        };
+        auto flag_passed = [&]() {
+          __syncwarp();
+          if (lane == 0) flag_store_release(flag_own, (unsigned)ph + 1);
+        };
+        auto release_acc = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_leader(&acc_empty[buf]);
+        };
+        const uint32_t t_base = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * 256 + 128 * grp);
+
+        // Poly: G's entries of the warp's chunks, by TMA into its staging tiles, once the phase
+        // before is written (the producer acquired it for the CTA).
+        int n_mine = 0;
+#pragma unroll
+        for (int kk = 0; kk < kOgChunks; ++kk) n_mine += mine(kk) ? 1 : 0;
+        const bool any = n_mine > 0 && m0 < p.m;
+        if (f.kind == kOrthPoly && any) {
+          const bool up = mbar_wait_bounded(ready, (uint32_t)ph & 1u, p.wait_budget, s_abort);
+          if (!__all_sync(0xFFFFFFFFu, up)) {
+            alive = false;
+            break;
+          }
+          ++g_issued;
+          if (lane == 0) {
+            bulk_wait_group_read<0>();   // the last tile's stores have read the staging tiles
+            fence_proxy_async_all();
+            mbar_arrive_expect_tx(g_bar, (uint32_t)(n_mine * kOgTileBytes));
+            for (int kk = 0; kk < kOgChunks; ++kk)
+              if (mine(kk)) tma_load_3d(stg + kk * kOgTileBytes, &maps.g_st, g_bar, n0 + 32 * kk, m0, b);
+          }
+          __syncwarp();
+        }
+        const bool got = mbar_wait_bounded(&acc_full[buf], (uint32_t)(j >> 1) & 1u, p.wait_budget, s_abort);
+        if (!__all_sync(0xFFFFFFFFu, got)) {
+          alive = false;
+          break;
+        }
+        tc_fence_after();
+        if (split) {
+          orth_pass_chunks(t_base, nch, part, parts, part_own);
+          flag_passed();
+          if (!others_ready()) {
+            alive = false;
+            break;
+          }
+        }
+        if (!any) {
+          release_acc();
+          continue;
+        }
+        if (f.kind == kOrthPoly) {
+          const bool here = mbar_wait_bounded(g_bar, g_used & 1u, p.wait_budget, s_abort);
+          if (!__all_sync(0xFFFFFFFFu, here)) {
+            alive = false;
+            break;
+          }
+          ++g_used;
+        } else {
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
+        }
+        const float alpha = f.kind == kOrthGram ? p.gram_alpha : 1.0f;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          uint32_t r[2][2][16];
+          orth_load_half(t_base + (uint32_t)(64 * half), nch - 2 * half, r);
+          if (half == 1) release_acc();
+          if (!mine(2 * half) && !mine(2 * half + 1)) continue;
+          if (split) {   // add the other parts' sums to its own, in part order
+#pragma unroll 1
+            for (int d = 0; d < parts; ++d) {
+              if (d == part) continue;
+              const float4 *src = part_own + (int64_t)(2 * (d - part)) * (kOgPartFloats / 4) + 2 * half * 8 * 32;
+              float4 pv[2][2][4];
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  pv[k][e >> 2][e & 3] = mine(2 * half + k) ? __ldcg(src + (8 * k + e) * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float4 v = pv[k][e >> 2][e & 3];
+                  uint32_t *a = &r[k][e >> 2][4 * (e & 3)];
+                  a[0] = __float_as_uint(__fadd_rn(__uint_as_float(a[0]), v.x));
+                  a[1] = __float_as_uint(__fadd_rn(__uint_as_float(a[1]), v.y));
+                  a[2] = __float_as_uint(__fadd_rn(__uint_as_float(a[2]), v.z));
+                  a[3] = __float_as_uint(__fadd_rn(__uint_as_float(a[3]), v.w));
+                }
+            }
+          }
+          // fp16 pairs in place (register 4g + e of [k][h], e = 2 (i % 2) + sub, i = 2g + e / 2),
+          // and to the staging tiles.  A chunk that is not this part's is packed too, its
+          // tile is not stored.
+          const uint32_t d_at = stg_u32 + (uint32_t)(2 * half * kOgTileBytes);
+          if (f.kind == kOrthPoly) {
+            const int diag = m0 + lr - (n0 + 64 * half + lc);   // row - column of the first entry
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                  uint32_t gv[4];
+                  ldmatrix_x4(d_at + (uint32_t)(k * kOgTileBytes) + swz64(16 * h + d_row, 2 * g + d_unit), gv);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const int d = diag + 16 * h + 8 * (e & 1) - 32 * k - 16 * g - 8 * (e >> 1);
+                    float gx, gy;
+                    unpack2<false>(gv[e], gx, gy);
+                    const float x = fmaf(p.c, __uint_as_float(r[k][h][8 * g + 2 * e]), p.b * gx) + (d == 0 ? p.a : 0.0f);
+                    const float y = fmaf(p.c, __uint_as_float(r[k][h][8 * g + 2 * e + 1]), p.b * gy) + (d == 1 ? p.a : 0.0f);
+                    r[k][h][4 * g + e] = pack2<false>(x, y);
+                  }
+                }
+            __syncwarp();   // every lane has its entries of G: P takes their places
+          } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  r[k][h][e] = pack2<false>(alpha * __uint_as_float(r[k][h][2 * e]), alpha * __uint_as_float(r[k][h][2 * e + 1]));
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                const uint32_t pk[4] = {r[k][h][4 * g], r[k][h][4 * g + 1], r[k][h][4 * g + 2], r[k][h][4 * g + 3]};
+                stmatrix_x4(d_at + (uint32_t)(k * kOgTileBytes) + swz64(16 * h + d_row, 2 * g + d_unit), pk);
+              }
+          auto store = [&](bool transposed) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {   // the TMA unit clips rows and columns past the matrix
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int kk = 2 * half + k;
+                if (!mine(kk)) continue;
+                if (transposed) tma_store_3d(mo, stg + kk * kOgTileBytes, m0, n0 + 32 * kk, b);
+                else tma_store_3d(mo, stg + kk * kOgTileBytes, n0 + 32 * kk, m0, b);
+              }
+              bulk_commit_group();
+            }
+          };
+          store(false);
+          if (below) {
+            if (lane == 0) bulk_wait_group_read<0>();
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                  const uint32_t pk[4] = {r[k][h][4 * g], r[k][h][4 * g + 1], r[k][h][4 * g + 2], r[k][h][4 * g + 3]};
+                  stmatrix_x4_trans(d_at + (uint32_t)(k * kOgTileBytes) + swz64(16 * g + t_row, 2 * h + t_unit), pk);
+                }
+            store(true);
+          }
+        }
+      }
+      __syncwarp();
+      if (alive && lane == 0) {   // this warp's stores of the phase are complete
+        bulk_wait_group<0>();
+        flag_add_release(p.counters + ew * kOgPhases + ph, 1u);
+      }
+    }
+    if (lane == 0) {
+      bulk_wait_group<0>();
+      if (g_used < g_issued) {   // after an abort, let the load of G in flight land
+        volatile int no_abort = 0;
+        mbar_wait_bounded(g_bar, g_used & 1u, kDrainBudget, &no_abort);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the peer's MMAs, copies and arrivals into this CTA are over
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------ the last product
+struct OrthLast {
+  int rows, cols;            // the matrices; tall: X holds their transposes
+  int num_kt;
+  int batch, tiles;          // tiles per matrix
+  uint64_t wait_budget;
+  float alpha;               // 1/s, or step/s
+  float keep;
+  float *w;                  // [batch][rows][cols]
+  uint16_t *out16;           // [batch][rows][cols]; UPDATE: may be null
+};
+
+constexpr int kOlEpiWarps = 16;
+constexpr int kOlThreads = 64 + 32 * kOlEpiWarps;
+constexpr int kOlStages = 6;
+constexpr int kOlSmem = kOlStages * kOgStageBytes + kOgBarBytes + 1024;
+
+// 32 rows of a column with pitch ld, `left` of them inside the matrix (the last one repeats).
+__device__ __forceinline__ void orth_load_rows(const float *src, int ld, int left, float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i, src += i < left ? ld : 0) v[i] = __ldcs(src);
+}
+
+// Lane = column of the matrix, accumulator column = row.  Persistent over 256 x 256 tiles, two
+// accumulators.  16 epilogue warps take 32 columns x 64 rows of the tile each, in two chunks of
+// 32 rows; the first chunk's W is loaded before the accumulator is ready, the second's before
+// the first is stored, so 64 KB of W per SM are in flight behind the main loop.  Bound, with
+// UPDATE, by memory: 10 bytes per entry.
+template <bool BF16, bool UPDATE, bool TALL>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOlThreads, 1)
+    orth_last_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                     const OrthLast p) {
+  constexpr int kStages = kOlStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kStages * kOgStageBytes);
+  uint64_t *full = bars;                       // [stages] leader: TMA (both CTAs) -> MMA
+  uint64_t *empty = bars + kStages;            // [stages] MMA -> this CTA's TMA
+  uint64_t *acc_full = bars + 2 * kStages;     // [2] MMA -> this CTA's epilogue
+  uint64_t *acc_empty = acc_full + 2;          // [2] leader: both epilogues -> MMA
+  uint64_t *drain = acc_empty + 2;
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(drain + 1);
+  volatile int *s_abort = reinterpret_cast<volatile int *>(s_tmem + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool is_leader = rank == 0;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int num_tiles = p.batch * p.tiles;
+  const int num_mt = (p.cols + 255) / 256;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 2 * kOlEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *s_abort = 0;
+    fence_mbarrier_init();
+    prefetch_tensormap(&tm_a);
+    prefetch_tensormap(&tm_b);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(s_tmem, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before any cross-CTA arrive or byte count
+  tc_fence_after();
+  const uint32_t tmem_base = *s_tmem;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  auto tile_at = [&](int tile, int &b, int &m0, int &n0) {
+    b = tile / p.tiles;
+    const int t = tile - b * p.tiles;
+    m0 = (t % num_mt) * 256;
+    n0 = (t / num_mt) * 256;
+  };
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------ producer (both CTAs)
+    uint32_t g = 0;
+    bool ok = true;
+    for (int tile = pair; ok && tile < num_tiles; tile += npairs) {
+      int b, m0, n0;
+      tile_at(tile, b, m0, n0);
+      const int a_row = m0 + (int)rank * 128, b_row = n0 + (int)rank * 128;
+      for (int kt = 0; kt < p.num_kt; ++kt, ++g) {
+        const int s = (int)(g % kStages);
+        if (!mbar_wait_bounded(&empty[s], ((g / kStages) & 1u) ^ 1u, p.wait_budget, s_abort)) {
+          ok = false;
+          break;
+        }
+        uint8_t *st = smem + s * kOgStageBytes;
+        if (is_leader) mbar_arrive_expect_tx(&full[s], 2 * kOgStageBytes);
+        // P K-major, X in two 64-column atoms of 64 rows.
+        if (TALL) {
+          tma_load_3d_pair(st, &tm_a, &full[s], kt * 64, a_row, b);
+          tma_load_3d_pair(st + 16384, &tm_b, &full[s], b_row, kt * 64, b);
+          tma_load_3d_pair(st + 24576, &tm_b, &full[s], b_row + 64, kt * 64, b);
+        } else {
+          tma_load_3d_pair(st, &tm_a, &full[s], a_row, kt * 64, b);
+          tma_load_3d_pair(st + 8192, &tm_a, &full[s], a_row + 64, kt * 64, b);
+          tma_load_3d_pair(st + 16384, &tm_b, &full[s], kt * 64, b_row, b);
+        }
+      }
+    }
+    // The leader's `full` barriers count both CTAs' bytes: let every copy land.
+    if (is_leader) {
+      for (uint32_t i = g > kStages ? g - kStages : 0; i < g; ++i) {
+        volatile int no_abort = 0;
+        mbar_wait_bounded(&full[i % kStages], (i / kStages) & 1u, kDrainBudget, &no_abort);
+      }
+    }
+  } else if (warp == 1 && lane == 0 && is_leader) {
+    // ----------------------------------------------------- MMA issuer (leader)
+    constexpr uint32_t idesc = make_idesc_dense(false, 256, 256) | (TALL ? 1u << 16 : 1u << 15);
+    const uint64_t a_desc0 = smem_desc(smem_u32(smem), TALL ? 16 : 8192, 1024, kSwizzle128B);
+    const uint64_t b_desc0 = smem_desc(smem_u32(smem + 16384), TALL ? 8192 : 16, 1024, kSwizzle128B);
+    uint32_t g = 0;
+    bool ok = true;
+    int j = 0;
+    for (int tile = pair; ok && tile < num_tiles; tile += npairs, ++j) {
+      const int buf = j & 1;
+      if (!(ok = mbar_wait_bounded(&acc_empty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, p.wait_budget, s_abort))) break;
+      tc_fence_after();
+      const uint32_t acc = tmem_base + (uint32_t)(buf * 256);
+      for (int kt = 0; kt < p.num_kt; ++kt, ++g) {
+        const int s = (int)(g % kStages);
+        if (!(ok = mbar_wait_bounded(&full[s], (g / kStages) & 1u, p.wait_budget, s_abort))) break;
+        tc_fence_after();
+        const uint64_t so = (uint64_t)((s * kOgStageBytes) >> 4);
+        // A K step of 16 moves 32 bytes along the rows, or, MN-major, 16 rows of 128 bytes.
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          tc_mma_f16_pair(acc, a_desc0 + so + kk * (TALL ? 2 : 2048 >> 4), b_desc0 + so + kk * (TALL ? 2048 >> 4 : 2),
+                          idesc, (kt != 0 || kk != 0) ? 1u : 0u);
+        tc_commit_pair(&empty[s], 0x3);
+      }
+      if (ok) tc_commit_pair(&acc_full[buf], 0x3);
+    }
+    if (!ok) {
+      tc_commit_pair(drain, 0x1);
+      volatile int no_abort = 0;
+      mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
+    }
+  } else if (warp >= 2) {
+    // ---------------------------------------------------- epilogue (both CTAs)
+    const int ew = warp - 2, grp = ew >> 2, q = warp & 3;
+    bool alive = true;
+    int j = 0;
+    for (int tile = pair; alive && tile < num_tiles; tile += npairs, ++j) {
+      int b, m0, n0;
+      tile_at(tile, b, m0, n0);
+      const int col = m0 + (int)rank * 128 + 32 * q + lane;
+      const int row0 = n0 + 64 * grp;
+      const int left = p.rows - row0;   // rows of the matrix from this warp's first on
+      const int64_t at = ((int64_t)b * p.rows + row0) * p.cols;
+      const float *w_src = p.w + at + min(col, p.cols - 1);   // loads past the last column repeat it
+      float pre[32];
+      if (UPDATE && left > 0) orth_load_rows(w_src, p.cols, left, pre);
+      const int buf = j & 1;
+      const bool got = mbar_wait_bounded(&acc_full[buf], (uint32_t)(j >> 1) & 1u, p.wait_budget, s_abort);
+      if (!__all_sync(0xFFFFFFFFu, got)) {
+        alive = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t t_base = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * 256 + 64 * grp);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(t_base + (uint32_t)(32 * k), r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));   // uses stay below the wait
+        if (k == 1) {   // the accumulator goes back to the MMA
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_leader(&acc_empty[buf]);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float acc = __uint_as_float(r[i]);
+          r[i] = __float_as_uint(UPDATE ? fmaf(-p.alpha, acc, p.keep * pre[i]) : p.alpha * acc);
+        }
+        if (UPDATE && k == 0 && left > 32) orth_load_rows(w_src + (int64_t)32 * p.cols, p.cols, left - 32, pre);
+        const int n_rows = col < p.cols ? left - 32 * k : 0;
+        float *w_at = p.w + at + (int64_t)(32 * k) * p.cols + col;
+        uint16_t *o_at = p.out16 + at + (int64_t)(32 * k) * p.cols + col;
+        const bool out = !UPDATE || p.out16 != nullptr;
+#pragma unroll
+        for (int i = 0; i < 32; ++i, w_at += p.cols, o_at += p.cols) {
+          if (i < n_rows) {
+            if (UPDATE) __stcs(w_at, __uint_as_float(r[i]));
+            if (out) *o_at = (uint16_t)f32_to_bits<BF16>(__uint_as_float(r[i]));
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the peer's MMAs, copies and arrivals into this CTA are over
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
+}  // namespace sp24

@@ -41,6 +41,72 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v) {
   return t;
 }
 
+// Rows of whole aligned 16-byte units, held in registers between the two passes: TPR threads
+// (a warp, or the block) per row, NV units of 8 entries per thread, so each entry is read
+// once and a thread has NV independent loads in flight.  rint(p) for |p| <= 2^22 is the low
+// byte of p + 1.5 2^23 (one fp32 addition rounding to even; the conversion instruction runs at
+// an eighth of its rate).
+template <bool BF16, bool MASKED, int TPR, int NV>
+__global__ void __launch_bounds__(kQuantThreads)
+    quantize_vec_kernel(const uint16_t *__restrict__ X, int64_t rows, int64_t cols, int64_t ldx,
+                        const uint8_t *__restrict__ idx, int8_t *__restrict__ q, float *__restrict__ scale) {
+  pdl_launch_dependents();
+  pdl_wait();
+  constexpr int kRows = kQuantThreads / TPR;
+  const int t = threadIdx.x % TPR;
+  const int nvec = (int)(cols >> 3);
+  for (int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR; r < rows; r += (int64_t)gridDim.x * kRows) {
+    const uint4 *x = reinterpret_cast<const uint4 *>(X + r * ldx);
+    uint4 v[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) v[k] = t + k * TPR < nvec ? __ldcs(x + t + k * TPR) : make_uint4(0u, 0u, 0u, 0u);
+    if (MASKED) {
+      const uint16_t *id = reinterpret_cast<const uint16_t *>(idx + (r >> 2) * (cols >> 2));
+      const int sh = 4 * (int)(r & 3);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        if (t + k * TPR >= nvec) continue;
+        const uint32_t two = __ldg(id + t + k * TPR);
+        uint32_t *e = reinterpret_cast<uint32_t *>(&v[k]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t keep = (uint32_t)g_tables.bits[(two >> (8 * h)) & 0xFFu] >> sh;
+          e[2 * h] &= ((keep & 1u) ? 0xFFFFu : 0u) | ((keep & 2u) ? 0xFFFF0000u : 0u);
+          e[2 * h + 1] &= ((keep & 4u) ? 0xFFFFu : 0u) | ((keep & 8u) ? 0xFFFF0000u : 0u);
+        }
+      }
+    }
+    uint32_t am = 0;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const uint32_t *e = reinterpret_cast<const uint32_t *>(&v[k]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) am = __vmaxu2(am, e[i] & 0x7FFF7FFFu);
+    }
+    am = max(am & 0xFFFFu, am >> 16);
+    am = TPR == 32 ? __reduce_max_sync(0xFFFFFFFFu, am) : block_max(am);
+    const float2 s = quant_scales<BF16>(am);
+    uint2 *out = reinterpret_cast<uint2 *>(q + r * cols);
+    const bool zero = s.y == 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const uint32_t *e = reinterpret_cast<const uint32_t *>(&v[k]);
+      uint32_t b[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        unpack2<BF16>(e[i], lo, hi);
+        b[2 * i] = __float_as_uint(__fadd_rn(__fmul_rn(lo, s.y), 12582912.0f));
+        b[2 * i + 1] = __float_as_uint(__fadd_rn(__fmul_rn(hi, s.y), 12582912.0f));
+      }
+      const uint32_t w0 = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+      const uint32_t w1 = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
+      if (t + k * TPR < nvec) __stcs(out + t + k * TPR, zero ? make_uint2(0u, 0u) : make_uint2(w0, w1));
+    }
+    if (t == 0) scale[r] = s.x;
+  }
+}
+
 // A block per row, any sizes and pitches.
 template <bool BF16, bool MASKED>
 __global__ void __launch_bounds__(kQuantThreads)

@@ -14,11 +14,12 @@
 #include <utility>
 
 #include "sp24.h"
-#include "gemm_nt.cuh"
+#include "gemm_i8.cuh"
 #include "gemm_sp.cuh"
 #include "mask_kernels.cuh"
 #include "mvue.cuh"
 #include "ortho.cuh"
+#include "ortho_gemm.cuh"
 #include "quant.cuh"
 
 namespace {
@@ -554,24 +555,23 @@ bool make_map_3d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t ou
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// CTA pairs of an instantiation that fit at once (and, once per device, its shared-memory opt-in).
-template <int MODE, int BN, bool BF16, bool GELU>
-int nt_pairs() {
-  constexpr int smem_bytes = NtGeom<MODE, BN>::kSmem;
-  auto kernel = sp24_gemm_nt_kernel<MODE, BN, BF16, GELU>;
+// CTA pairs of a kernel that fit at once (and, once per device, its shared-memory opt-in);
+// 0: the set-up failed, -1: no device.
+template <auto KERNEL, int THREADS, int SMEM>
+int pairs_of() {
   static PerDevice cache;
   const int dev = current_device();
   if (dev < 0) return -1;
   std::call_once(cache.once[dev], [&] {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes) != cudaSuccess) {
+    if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess) {
       cudaGetLastError();
       cache.value[dev] = 0;
       return;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (unsigned)(sm_count() / 2));
-    cfg.blockDim = dim3(kNtThreads);
-    cfg.dynamicSmemBytes = smem_bytes;
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = 2;
@@ -580,37 +580,22 @@ int nt_pairs() {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&n, KERNEL, &cfg) != cudaSuccess || n <= 0) {
       cudaGetLastError();
-      n = sm_count() / 2;
+      n = 0;
     }
     cache.value[dev] = n;
   });
   return cache.value[dev];
 }
 
-template <int MODE, int BN, bool BF16 = false, bool GELU = false>
-sp24_status launch_nt(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &to, NtArgs args,
-                      cudaStream_t stream) {
-  using G = NtGeom<MODE, BN>;
-  const int pairs = nt_pairs<MODE, BN, BF16, GELU>();
-  if (pairs <= 0) return pairs == 0 ? SP24_ERR_CUDA : SP24_ERR_NO_DEVICE;
-  const int64_t tiles = G::kSym ? nt_sym_tiles(args.M, BN)
-                                : ((int64_t)(args.M + 255) / 256) * (((int64_t)args.N + BN - 1) / BN);
-  if (tiles * args.batch > INT32_MAX) return SP24_ERR_UNSUPPORTED_SHAPE;
-  args.tiles = (int)tiles;
-  args.wait_budget = g_wait_budget.load();
-  const int64_t total = tiles * args.batch;
-  const int grid = (int)(total < pairs ? total : pairs);
-  return launch_pdl(sp24_gemm_nt_kernel<MODE, BN, BF16, GELU>, dim3(2 * grid), dim3(kNtThreads), G::kSmem, stream, ta,
-                    tb, to, args);
-}
-
-// Newton-Schulz on the short side m of every matrix, n the long side; the workspace holds the
-// norm's partial sums, two iterates [count][m][ldx], G and P [count][m][ldm] (fp16).
+// Newton-Schulz on the short side m of every matrix, n the long side.  The workspace holds
+// counters, the norm's partial sums, two iterates [count][m][ldx], G and P [count][m][ldm]
+// (fp16), and the split tiles' partial sums.
 struct OrthPlan {
   int64_t count, rows, cols, m, n, ldx, ldm;
-  size_t part, x0, x1, gram, poly, total;   // byte offsets
+  int64_t sym_tiles, tiles;                 // 256 x 256 tiles of the symmetric products and of P X, per matrix
+  size_t counters, norm, x0, x1, gram, poly, part, total;   // byte offsets
   bool tall;
 };
 
@@ -634,12 +619,21 @@ sp24_status orth_plan(int64_t count, int64_t rows, int64_t cols, OrthPlan *p) {
     return here;
   };
   const size_t bx = (size_t)count * p->m * p->ldx * 2, bm = (size_t)count * p->m * p->ldm * 2;
-  p->part = take((size_t)count * kOrthMaxBlocks * sizeof(double));
+  const int64_t mb = (p->m + 255) / 256, nb = (p->n + 255) / 256;
+  p->sym_tiles = mb * (mb + 1) / 2;
+  p->tiles = mb * nb;
+  if (count * (p->sym_tiles > p->tiles ? p->sym_tiles : p->tiles) > INT32_MAX) return SP24_ERR_UNSUPPORTED_SHAPE;
+  // A launch has at most kOgMaxSplit pairs per tile, and at most kOgMaxPairs.
+  const int64_t want = kOgMaxSplit * count * p->tiles;
+  const int64_t slots = want < kOgMaxPairs ? want : kOgMaxPairs;
+  p->counters = take(kOgCounters * sizeof(unsigned));
+  p->norm = take((size_t)count * kOrthMaxBlocks * sizeof(double));
   p->x0 = take(bx);
   p->x1 = take(bx);
   p->gram = take(bm);
   p->poly = take(bm);
-  p->total = at;
+  p->part = take((size_t)(2 * slots * kOgPartFloats) * sizeof(float));
+  p->total = count == 0 || p->m == 0 ? 0 : at;
   return SP24_OK;
 }
 
@@ -653,45 +647,95 @@ struct OrthOut {
   bool bf16;
 };
 
-template <bool BF16>
-sp24_status launch_orth_last(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &to, const NtArgs &args,
+// Parts that a tail of r tiles of kt K stages on P pairs is split into: the least of the
+// measured times of a tile's main loop (0.38 us a stage), of its epilogue (2.8 us, shared by
+// the parts) and, for s > 1, of the exchange (1.5 us to wait, 5.2 us (s-1)/s to write and add).
+int orth_split(int64_t r, int64_t kt, int64_t P) {
+  int best = 1;
+  double least = 0.38 * (double)kt + 2.8;
+  for (int64_t s = 2; s <= kOgMaxSplit && s <= kt && r * s <= P; ++s) {
+    const double t = 0.38 * (double)((kt + s - 1) / s) + 2.8 / (double)s + 1.5 + 5.2 * (double)(s - 1) / (double)s;
+    if (t < least) {
+      least = t;
+      best = (int)s;
+    }
+  }
+  return best;
+}
+
+sp24_status launch_orth_products(const OrthMaps &maps, OrthProducts p, cudaStream_t stream) {
+  int64_t P = pairs_of<orth_products_kernel, kOgThreads, kOgSmem>();
+  if (P <= 0) return P == 0 ? SP24_ERR_CUDA : SP24_ERR_NO_DEVICE;
+  if (P > kOgMaxPairs) P = kOgMaxPairs;
+  const int64_t all[3] = {(int64_t)p.batch * p.sym_tiles, (int64_t)p.batch * p.sym_tiles, (int64_t)p.batch * p.tiles};
+  const int64_t kt[3] = {(p.n + 63) / 64, (p.m + 63) / 64, (p.m + 63) / 64};
+  int64_t grid = 0;   // pairs: as many as the phase that uses most
+  for (int k = 0; k < 3; ++k) {
+    const int64_t use = all[k] >= P ? P : all[k] * orth_split(all[k], kt[k], P);
+    if (use > grid) grid = use;
+  }
+  for (int k = 0; k < 3; ++k) {
+    const int64_t tail = all[k] % grid;
+    p.split[k] = tail ? orth_split(tail, kt[k], grid) : 1;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (unsigned)grid);
+  cfg.blockDim = dim3(kOgThreads);
+  cfg.dynamicSmemBytes = kOgSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;   // its CTAs wait for one another: all are resident, or none starts
+  attr.id = cudaLaunchAttributeCooperative;
+  attr.val.cooperative = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, orth_products_kernel, maps, p) != cudaSuccess) {
+    cudaGetLastError();
+    return SP24_ERR_CUDA;
+  }
+  return SP24_OK;
+}
+
+template <bool BF16, bool UPDATE, bool TALL>
+sp24_status launch_orth_last_t(const CUtensorMap &p_rows, const CUtensorMap &x_cols, const OrthLast &p, cudaStream_t s) {
+  constexpr auto kernel = orth_last_kernel<BF16, UPDATE, TALL>;
+  const int pairs = pairs_of<kernel, kOlThreads, kOlSmem>();
+  if (pairs <= 0) return pairs == 0 ? SP24_ERR_CUDA : SP24_ERR_NO_DEVICE;
+  const int64_t tiles = (int64_t)p.batch * p.tiles;
+  const int grid = (int)(tiles < pairs ? tiles : pairs);
+  return launch_pdl(kernel, dim3(2 * grid), dim3(kOlThreads), kOlSmem, s, TALL ? p_rows : x_cols, TALL ? x_cols : p_rows, p);
+}
+
+template <bool BF16, bool UPDATE>
+sp24_status launch_orth_last(const CUtensorMap &p_rows, const CUtensorMap &x_cols, bool tall, const OrthLast &p,
                              cudaStream_t s) {
-  return args.w ? launch_nt<kNtMuon, 256, BF16>(ta, tb, to, args, s) : launch_nt<kNtOrth, 256, BF16>(ta, tb, to, args, s);
+  return tall ? launch_orth_last_t<BF16, UPDATE, true>(p_rows, x_cols, p, s)
+              : launch_orth_last_t<BF16, UPDATE, false>(p_rows, x_cols, p, s);
 }
 
 sp24_status run_orth(const OrthPlan &pl, OrthSrc src, const OrthOut &o, int steps, float eps, void *workspace,
                      cudaStream_t stream) {
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  double *part = reinterpret_cast<double *>(ws + pl.part);
+  unsigned *counters = reinterpret_cast<unsigned *>(ws + pl.counters);
+  double *part = reinterpret_cast<double *>(ws + pl.norm);
   __half *xb[2] = {reinterpret_cast<__half *>(ws + pl.x0), reinterpret_cast<__half *>(ws + pl.x1)};
   void *gram = ws + pl.gram, *poly = ws + pl.poly;
   const uint64_t px = (uint64_t)pl.ldx * 2, pm = (uint64_t)pl.ldm * 2;
   const uint64_t m = (uint64_t)pl.m, n = (uint64_t)pl.n, bt = (uint64_t)pl.count;
   const CUtensorMapSwizzle s128 = CU_TENSOR_MAP_SWIZZLE_128B, s64 = CU_TENSOR_MAP_SWIZZLE_64B;
-  constexpr int kSymBN = 128, kApplyBN = 256;
-  // x_rows: X as a K-major operand; x_half: the same with a CTA's half of the columns' tile;
-  // x_cols: X as the MN-major operand; *_st: 32 x 32 store tiles.
-  CUtensorMap x_rows[2], x_half[2], x_cols[2], x_st[2], g_rows, g_half, g_st, p_rows, p_st, out_st;
+  // rows: a K-major operand; cols: the MN-major one; st: 32 x 32 store tiles.
+  OrthMaps maps;
   bool ok = true;
   for (int i = 0; i < 2; ++i)
-    ok = ok && make_map_3d(&x_rows[i], xb[i], n, m, bt, px, m * px, 64, 128, s128) &&
-         make_map_3d(&x_half[i], xb[i], n, m, bt, px, m * px, 64, kSymBN / 2, s128) &&
-         make_map_3d(&x_cols[i], xb[i], n, m, bt, px, m * px, 64, 64, s128) &&
-         make_map_3d(&x_st[i], xb[i], n, m, bt, px, m * px, 32, 32, s64);
-  ok = ok && make_map_3d(&g_rows, gram, m, m, bt, pm, m * pm, 64, 128, s128) &&
-       make_map_3d(&g_half, gram, m, m, bt, pm, m * pm, 64, kSymBN / 2, s128) &&
-       make_map_3d(&g_st, gram, m, m, bt, pm, m * pm, 32, 32, s64) &&
-       make_map_3d(&p_rows, poly, m, m, bt, pm, m * pm, 64, 128, s128) &&
-       make_map_3d(&p_st, poly, m, m, bt, pm, m * pm, 32, 32, s64);
+    ok = ok && make_map_3d(&maps.x_rows[i], xb[i], n, m, bt, px, m * px, 64, 128, s128) &&
+         make_map_3d(&maps.x_cols[i], xb[i], n, m, bt, px, m * px, 64, 64, s128) &&
+         make_map_3d(&maps.x_st[i], xb[i], n, m, bt, px, m * px, 32, 32, s64);
+  ok = ok && make_map_3d(&maps.g_rows, gram, m, m, bt, pm, m * pm, 64, 128, s128) &&
+       make_map_3d(&maps.g_st, gram, m, m, bt, pm, m * pm, 32, 32, s64) &&
+       make_map_3d(&maps.p_rows, poly, m, m, bt, pm, m * pm, 64, 128, s128) &&
+       make_map_3d(&maps.p_st, poly, m, m, bt, pm, m * pm, 32, 32, s64);
   if (!ok) return SP24_ERR_CUDA;
-  const uint64_t out_row = (uint64_t)pl.cols * 2;
-  const bool tma_out = !o.w && out_row % 16 == 0 && aligned16(o.out16);
-  out_st = p_st;   // not used unless tma_out
-  if (tma_out && !make_map_3d(&out_st, o.out16, (uint64_t)pl.cols, (uint64_t)pl.rows, bt, out_row, out_row * pl.rows, 32,
-                              32, s64))
-    return SP24_ERR_CUDA;
 
-  // Scale of the iterate: a power of two near sqrt(n) (gemm_nt.cuh).
+  // Scale of the iterate: a power of two near sqrt(n) (ortho_gemm.cuh).
   int e = 0;
   while ((int64_t(1) << (2 * (e + 1))) <= pl.n) ++e;
   const float s = (float)(1 << e);
@@ -707,49 +751,51 @@ sp24_status run_orth(const OrthPlan &pl, OrthSrc src, const OrthOut &o, int step
   sp24_status st = vec ? launch_pdl(orth_sumsq_kernel<true>, grid1, dim3(kOrthThreads), 0, stream, src, part)
                        : launch_pdl(orth_sumsq_kernel<false>, grid1, dim3(kOrthThreads), 0, stream, src, part);
   if (st != SP24_OK) return st;
-  const int64_t row_tiles = (pl.rows + kOrthTile - 1) / kOrthTile;
-  const dim3 grid2((unsigned)((pl.cols + kOrthTile - 1) / kOrthTile), (unsigned)(row_tiles < 65535 ? row_tiles : 65535),
-                   (unsigned)pl.count);
-  st = pl.tall ? launch_pdl(orth_scale_kernel<true>, grid2, dim3(kOrthThreads), 0, stream, src, part, (int)blocks, s, eps,
-                            xb[0], pl.ldx, row_tiles)
-               : launch_pdl(orth_scale_kernel<false>, grid2, dim3(kOrthThreads), 0, stream, src, part, (int)blocks, s, eps,
-                            xb[0], pl.ldx, row_tiles);
+  const int64_t col_tiles = (pl.cols + kOrthTile - 1) / kOrthTile;
+  const int64_t tiles = col_tiles * ((pl.rows + kOrthTile - 1) / kOrthTile);
+  int64_t per = (8 * (int64_t)sm_count() + pl.count - 1) / pl.count;   // eight blocks of 256 threads an SM
+  if (per > tiles) per = tiles;
+  const dim3 grid2((unsigned)per, (unsigned)pl.count);
+  const bool quads = src.cols % 4 == 0 && src.ld % 4 == 0 && src.stride % 4 == 0 && aligned16(src.g) &&
+                     (!src.m || aligned16(src.m));
+  auto scale = pl.tall ? (quads ? orth_scale_kernel<true, true> : orth_scale_kernel<true, false>)
+                       : (quads ? orth_scale_kernel<false, true> : orth_scale_kernel<false, false>);
+  st = launch_pdl(scale, grid2, dim3(kOrthThreads), 0, stream, src, part, (int)blocks, s, eps, xb[0], pl.ldx, col_tiles,
+                  tiles, counters, kOgCounters);
   if (st != SP24_OK) return st;
 
-  NtArgs base = {};
-  base.M = (int)pl.m;
-  base.batch = (int)pl.count;
-  base.a = kNsA;
-  base.b = kNsB;
-  base.c = kNsC;
-  base.gram = static_cast<const uint16_t *>(gram);
-  base.gram_ld = pl.ldm;
-  for (int k = 0; k < steps; ++k) {
-    const int in = k & 1;
-    NtArgs a = base;
-    a.N = (int)pl.m;
-    a.num_kt = (int)((pl.n + 63) / 64);
-    a.alpha = 1.0f / (s * s);
-    if ((st = launch_nt<kNtGram, kSymBN>(x_rows[in], x_half[in], g_st, a, stream)) != SP24_OK) return st;
-    a.num_kt = (int)((pl.m + 63) / 64);
-    if ((st = launch_nt<kNtPoly, kSymBN>(g_rows, g_half, p_st, a, stream)) != SP24_OK) return st;
-    a.N = (int)pl.n;
-    if (k + 1 < steps) {
-      st = launch_nt<kNtApply, kApplyBN>(p_rows, x_cols[in], x_st[1 - in], a, stream);
-    } else {
-      a.out16 = o.out16;
-      a.w = o.w;
-      a.keep = o.keep;
-      a.alpha = (o.w ? o.step : 1.0f) / s;
-      a.tall = pl.tall ? 1 : 0;
-      a.tma_out = tma_out ? 1 : 0;
-      a.vec = !pl.tall && pl.n % 2 == 0 && aligned_to(o.w, 8) && aligned_to(o.out16, 4) ? 1 : 0;
-      st = o.bf16 ? launch_orth_last<true>(p_rows, x_cols[in], out_st, a, stream)
-                  : launch_orth_last<false>(p_rows, x_cols[in], out_st, a, stream);
-    }
-    if (st != SP24_OK) return st;
-  }
-  return SP24_OK;
+  OrthProducts p = {};
+  p.m = (int)pl.m;
+  p.n = (int)pl.n;
+  p.batch = (int)pl.count;
+  p.phases = 3 * steps - 1;
+  p.sym_tiles = (int)pl.sym_tiles;
+  p.tiles = (int)pl.tiles;
+  p.wait_budget = g_wait_budget.load();
+  p.gram_alpha = 1.0f / (s * s);
+  p.a = kNsA;
+  p.b = kNsB;
+  p.c = kNsC;
+  p.part = reinterpret_cast<float *>(ws + pl.part);
+  p.counters = counters;
+  if ((st = launch_orth_products(maps, p, stream)) != SP24_OK) return st;
+  OrthLast l = {};
+  l.rows = (int)pl.rows;
+  l.cols = (int)pl.cols;
+  l.num_kt = (int)((pl.m + 63) / 64);
+  l.batch = (int)pl.count;
+  l.tiles = (int)pl.tiles;
+  l.wait_budget = p.wait_budget;
+  l.alpha = (o.w ? o.step : 1.0f) / s;
+  l.keep = o.keep;
+  l.w = o.w;
+  l.out16 = o.out16;
+  const CUtensorMap &x_cols = maps.x_cols[(steps - 1) & 1];
+  if (o.bf16)
+    return o.w ? launch_orth_last<true, true>(maps.p_rows, x_cols, pl.tall, l, stream)
+               : launch_orth_last<true, false>(maps.p_rows, x_cols, pl.tall, l, stream);
+  return o.w ? launch_orth_last<false, true>(maps.p_rows, x_cols, pl.tall, l, stream)
+             : launch_orth_last<false, false>(maps.p_rows, x_cols, pl.tall, l, stream);
 }
 
 sp24_status validate_orth(const OrthPlan &pl, int steps, float eps, const void *workspace, size_t workspace_bytes) {
@@ -765,41 +811,63 @@ sp24_status validate_orth(const OrthPlan &pl, int steps, float eps, const void *
 // multiple of 16.
 constexpr int64_t kMaxI8K = 131056;
 
+template <int BN, bool BF16, bool GELU>
+sp24_status launch_i8_pair(const int8_t *Xq, int64_t T, int64_t K, const int8_t *Wq, int64_t N, void *Y,
+                           const float *sx, const float *sw, cudaStream_t s) {
+  using G = I8Geom<BN>;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  CUtensorMap tw, tx, ty;
+  if (!make_map_2d(&tw, Wq, (uint64_t)K, (uint64_t)N, (uint64_t)K, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B, u8) ||
+      !make_map_2d(&tx, Xq, (uint64_t)K, (uint64_t)T, (uint64_t)K, 128, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B, u8) ||
+      !make_map_2d(&ty, Y, (uint64_t)N, (uint64_t)T, (uint64_t)N * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+    return SP24_ERR_CUDA;
+  constexpr auto kernel = gemm_i8_kernel<BN, BF16, GELU>;
+  const int pairs = pairs_of<kernel, kI8Threads, G::kSmem>();
+  if (pairs <= 0) return pairs == 0 ? SP24_ERR_CUDA : SP24_ERR_NO_DEVICE;
+  const int64_t tiles = ((N + 255) / 256) * ((T + BN - 1) / BN);
+  if (tiles > INT32_MAX) return SP24_ERR_UNSUPPORTED_SHAPE;
+  const int grid = (int)(tiles < pairs ? tiles : pairs);
+  return launch_pdl(kernel, dim3(2 * grid), dim3(kI8Threads), G::kSmem, s, tw, tx, ty, (int)N, (int)T,
+                    (int)((K + 127) / 128), (uint64_t)g_wait_budget.load(), sw, sx);
+}
+
 template <bool BF16, bool GELU>
 sp24_status launch_i8(const int8_t *Xq, int64_t T, int64_t K, const int8_t *Wq, int64_t N, void *Y, const float *sx,
                       const float *sw, cudaStream_t s) {
-  const CUtensorMapSwizzle s128 = CU_TENSOR_MAP_SWIZZLE_128B;
-  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-  NtArgs a = {};
-  a.M = (int)N;
-  a.N = (int)T;
-  a.num_kt = (int)((K + 127) / 128);
-  a.batch = 1;
-  a.row_scale = sw;
-  a.col_scale = sx;
-  const int64_t mt = (N + 255) / 256;
-  const int bn = mt * ((T + 255) / 256) >= sm_count() / 2 ? 256 : (T > 64 ? 128 : 64);
-  CUtensorMap ta, tb, to;
-  if (!make_map_3d(&ta, Wq, (uint64_t)K, (uint64_t)N, 1, (uint64_t)K, (uint64_t)K * N, 128, 128, s128, u8) ||
-      !make_map_3d(&tb, Xq, (uint64_t)K, (uint64_t)T, 1, (uint64_t)K, (uint64_t)K * T, 128, (uint32_t)(bn / 2), s128, u8) ||
-      !make_map_3d(&to, Y, (uint64_t)N, (uint64_t)T, 1, (uint64_t)N * 2, (uint64_t)N * T * 2, 32, 32,
-                   CU_TENSOR_MAP_SWIZZLE_64B))
-    return SP24_ERR_CUDA;
-  switch (bn) {
-    case 256: return launch_nt<kNtI8, 256, BF16, GELU>(ta, tb, to, a, s);
-    case 128: return launch_nt<kNtI8, 128, BF16, GELU>(ta, tb, to, a, s);
-    default: return launch_nt<kNtI8, 64, BF16, GELU>(ta, tb, to, a, s);
+  if (((N + 255) / 256) * ((T + 255) / 256) >= sm_count() / 2)
+    return launch_i8_pair<256, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);
+  return launch_i8_pair<128, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);
+}
+
+// A warp per row holds the row in registers (up to 6144 entries); longer rows, and a matrix
+// of few rows, take a block per row (up to 8192 in registers); the rest re-reads its rows.
+template <bool BF16, bool MASKED>
+sp24_status launch_quant_t(const uint16_t *X, int64_t rows, int64_t cols, int64_t ldx, const uint8_t *idx, int8_t *q,
+                           float *scale, cudaStream_t s) {
+  const int64_t vecs = cols / 8;
+  const bool vec = cols % 8 == 0 && ldx % 8 == 0 && aligned_to(idx, 2);
+  const int64_t warp_blocks = (rows + kQuantThreads / 32 - 1) / (kQuantThreads / 32);
+  auto go = [&](auto kernel, int64_t blocks) {
+    return launch_pdl(kernel, dim3((unsigned)(blocks < INT32_MAX ? blocks : INT32_MAX)), dim3(kQuantThreads), 0, s, X,
+                      rows, cols, ldx, idx, q, scale);
+  };
+  if (vec && vecs > 0 && vecs <= 4 * kQuantThreads && (rows < 4 * (int64_t)sm_count() || vecs > 24 * 32))
+    return vecs <= kQuantThreads ? go(quantize_vec_kernel<BF16, MASKED, kQuantThreads, 1>, rows)
+                                 : go(quantize_vec_kernel<BF16, MASKED, kQuantThreads, 4>, rows);
+  if (vec && vecs > 0 && vecs <= 24 * 32) {
+    if (vecs <= 4 * 32) return go(quantize_vec_kernel<BF16, MASKED, 32, 4>, warp_blocks);
+    if (vecs <= 8 * 32) return go(quantize_vec_kernel<BF16, MASKED, 32, 8>, warp_blocks);
+    if (vecs <= 16 * 32) return go(quantize_vec_kernel<BF16, MASKED, 32, 16>, warp_blocks);
+    return go(quantize_vec_kernel<BF16, MASKED, 32, 24>, warp_blocks);
   }
+  return go(quantize_rows_kernel<BF16, MASKED>, rows);
 }
 
 template <bool BF16>
 sp24_status launch_quant(const uint16_t *X, int64_t rows, int64_t cols, int64_t ldx, const uint8_t *idx, int8_t *q,
                          float *scale, cudaStream_t s) {
-  const unsigned grid = (unsigned)(rows < INT32_MAX ? rows : INT32_MAX);
-  return idx ? launch_pdl(quantize_rows_kernel<BF16, true>, dim3(grid), dim3(kQuantThreads), 0, s, X, rows, cols, ldx, idx,
-                          q, scale)
-             : launch_pdl(quantize_rows_kernel<BF16, false>, dim3(grid), dim3(kQuantThreads), 0, s, X, rows, cols, ldx,
-                          idx, q, scale);
+  return idx ? launch_quant_t<BF16, true>(X, rows, cols, ldx, idx, q, scale, s)
+             : launch_quant_t<BF16, false>(X, rows, cols, ldx, idx, q, scale, s);
 }
 
 }  // namespace

@@ -24,12 +24,12 @@ def test_workspace_size_covers_its_parts(count, rows, cols):
     pad = lambda v: -(-v // 8) * 8
     need = 2 * (2 * count * m * pad(n)) + 2 * (2 * count * m * pad(m))
     got = sp.sp24_orthogonalize_size(rows, cols, count)
-    assert need <= got <= need + count * (1 << 16) + (1 << 16)
+    assert need <= got <= need + count * (1 << 16) + 2 * 80 * (1 << 17) + (1 << 16)   # + split tiles' partial sums
     assert sp.sp24_orthogonalize_size(cols, rows, count) == got
 
 
 def test_sizes_that_are_not_taken():
-    assert sp.sp24_orthogonalize_size(0, 64) >= 0
+    assert sp.sp24_orthogonalize_size(0, 64) == sp.sp24_orthogonalize_size(64, 64, 0) == 0
     for args in ((-1, 64, 64), (1, -1, 64), (1, 64, -1)):
         out = ctypes.c_size_t(0)
         assert _raw("sp24_orthogonalize_size", *args, ctypes.byref(out)) == E["SP24_ERR_INVALID_ARG"]
@@ -169,7 +169,7 @@ def test_valid_calls_without_a_device_report_no_device():
 def test_tile_numbering_of_the_symmetric_products():
     """Every block on and below the diagonal once, none above: the kernel's numbering restated."""
     for m in (1, 100, 128, 129, 256, 257, 700, 1600, 5000):
-        for bn in (128, 256):
+        for bn in (256,):
             R, rb, cb = 256 // bn, -(-m // 256), -(-m // bn)
             total = R * rb * (rb - 1) // 2 + min(cb, R * rb)
             seen = set()
