@@ -467,13 +467,16 @@ def _one_device(*ts):
 
 
 def _call_on(device, fn: str, stream, *args):
-    """Calls the entry point with `device` current, on `stream` or that device's current stream."""
+    """Calls the entry point with `device` current, on `stream` or that device's current stream.
+    (The raw handle of the current stream: building a torch.cuda.Stream around it takes longer
+    than a small kernel.)"""
     import torch
-    if torch.cuda.current_device() != device.index:
+    index = device.index
+    if torch.cuda.current_device() != index:
         with torch.cuda.device(device):
             return _call_on(device, fn, stream, *args)
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    status = getattr(_lib, fn)(*args, s.cuda_stream)
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    status = getattr(_lib, fn)(*args, handle)
     if status != 0:
         raise Sp24Error(fn, status)
 
@@ -486,10 +489,10 @@ def _stack3(t, name: str):
 
 
 def _out_code(t, name: str) -> int:
-    import torch
-    if t.dtype not in (torch.float16, torch.bfloat16):
-        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    return _dtype_code(t)
+    try:
+        return _dtype_code(t)
+    except TypeError:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}") from None
 
 
 def sp24_orthogonalize_size(rows: int, cols: int, count: int = 1) -> int:
@@ -548,14 +551,13 @@ def sp24_quantize_rows(X, q, scale, idx=None, stream=None):
     idx [R/4, C/4] (uint8) X is a weight and the entries its mask prunes count as 0."""
     import torch
     _need_rowmajor(q, scale, idx, pitched=(X,))
-    R, C = _shape2(X, "X")
+    R, C = X.shape
     code = _dtype_code(X)
     _expect(q, "q", torch.int8, R * C)
     _expect(scale, "scale", torch.float32, R)
     _expect(idx, "idx", torch.uint8, (R // 4) * (C // 4))
-    device = _one_device(X, q, scale, idx)
-    _call_on(device, "sp24_quantize_rows", stream, _ptr(X), code, R, C, X.stride(0) if R > 1 else C, _ptr(idx), _ptr(q),
-             _ptr(scale))
+    _call_on(_one_device(X, q, scale, idx), "sp24_quantize_rows", stream, X.data_ptr(), code, R, C,
+             X.stride(0) if R > 1 else C, None if idx is None else idx.data_ptr(), q.data_ptr(), scale.data_ptr())
 
 
 def sp24_gemm_i8(Xq, sx, Wq, sw, Y, epi=None, stream=None):
@@ -567,15 +569,17 @@ def sp24_gemm_i8(Xq, sx, Wq, sw, Y, epi=None, stream=None):
     N, K2 = _shape2(Wq, "Wq")
     if K2 != K:
         raise ValueError(f"Wq has {K2} columns, Xq has {K}")
-    _expect(Xq, "Xq", torch.int8, T * K)
-    _expect(Wq, "Wq", torch.int8, N * K)
+    # (as _expect, which names what is wrong; this is the one call here whose time a token's decoding sees)
+    if Xq.dtype != torch.int8 or Wq.dtype != torch.int8:
+        _expect(Xq, "Xq", torch.int8, T * K)
+        _expect(Wq, "Wq", torch.int8, N * K)
     _expect(sx, "sx", torch.float32, T)
     _expect(sw, "sw", torch.float32, N)
     code = _out_code(Y, "Y")
-    _expect(Y, "Y", Y.dtype, T * N)
-    device = _one_device(Xq, sx, Wq, sw, Y)
-    _call_on(device, "sp24_gemm_i8", stream, _ptr(Xq), _ptr(sx), T, K, _ptr(Wq), _ptr(sw), N, code, _ptr(Y),
-             EPILOGUES[epi])
+    if Y.numel() < T * N:
+        _expect(Y, "Y", Y.dtype, T * N)
+    _call_on(_one_device(Xq, sx, Wq, sw, Y), "sp24_gemm_i8", stream, Xq.data_ptr(), sx.data_ptr(), T, K, Wq.data_ptr(),
+             sw.data_ptr(), N, code, Y.data_ptr(), EPILOGUES[epi])
 
 
 def sp24_device_status(stream=None) -> int:

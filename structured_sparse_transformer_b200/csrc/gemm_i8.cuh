@@ -242,4 +242,252 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
   }
 }
 
+// ------------------------------------------------------------------ few tokens
+// Up to 128 tokens: bound by reading Wq (and, for small ones, by latency), so the work is
+// spread over the weight alone.  A cluster of S CTAs (S = 1, 2, 4 or 8) computes 128 features x
+// all tokens, each CTA an S-th of K: M = 128, N = TP MMAs (cta_group::1) on tiles that one
+// thread loads as fast as the ring of stages takes them.  The 32-bit integer partial sums
+// meet through distributed shared memory: each CTA leaves its own in shared memory, and CTA r
+// adds all of them for tokens r, r + S, ..., scales and stores (integer sums: the order does
+// not matter).
+// At T = 1, K = 1600, N = 6400 the two-CTA tile above took 7.1 us with 25 CTA pairs reading.
+constexpr int kI8sThreads = 192;                       // producer, MMA, four epilogue warps
+constexpr int kI8sMaxStages = 8;
+
+template <int TP>
+struct I8sGeom {
+  static constexpr int kSmemW = 128 * 128;
+  static constexpr int kStageBytes = kSmemW + TP * 128;
+  static constexpr int kPartBytes = TP * 128 * 4;      // partial sums [token][feature], over the stages
+  static constexpr int kBarBytes = 256;
+  static constexpr int smem_for(int stages) {
+    return (stages * kStageBytes > kPartBytes ? stages * kStageBytes : kPartBytes) + kBarBytes + 1024;
+  }
+  static constexpr int kMost = (232448 - kBarBytes - 1024) / kStageBytes;
+  static constexpr int kStagesMost = kMost < kI8sMaxStages ? kMost : kI8sMaxStages;
+  static_assert(TP == 16 || TP == 32 || TP == 64 || TP == 128, "token tiles");
+  static_assert(smem_for(kStagesMost) <= 232448 && 8 * (2 * kI8sMaxStages + 2) + 16 <= kBarBytes, "shared memory per CTA");
+};
+
+// Dense 8-bit integer MMA of one CTA (M = 128).
+__device__ __forceinline__ void tc_mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 32 lanes x 16 columns: lane i of the warp receives its tensor-memory lane's columns.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// The word at this shared-memory address in CTA `cta` of the cluster.
+__device__ __forceinline__ int ld_cluster_s32(uint32_t saddr, uint32_t cta) {
+  uint32_t remote;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(saddr), "r"(cta));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+  return v;
+}
+
+template <int TP, bool BF16, bool GELU>
+__global__ void __launch_bounds__(kI8sThreads)
+    gemm_i8_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, int N, int T,
+                       int num_kt, int split, int stages, uint64_t wait_budget, const float *__restrict__ sw,
+                       const float *__restrict__ sx, uint16_t *__restrict__ Y) {
+  using G = I8sGeom<TP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int body = max(stages * G::kStageBytes, G::kPartBytes);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + body);   // [stages] TMA -> MMA
+  uint64_t *empty = full + kI8sMaxStages;                       // [stages] MMA -> TMA
+  uint64_t *acc_full = empty + kI8sMaxStages;                   // MMA -> epilogue
+  uint64_t *drain = acc_full + 1;
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(drain + 1);
+  volatile int *s_abort = reinterpret_cast<volatile int *>(s_tmem + 1);
+  int *part = reinterpret_cast<int *>(smem);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % split;
+  const int f0 = (blockIdx.x / split) * 128;
+  const int kb = (int)((int64_t)rank * num_kt / split), ke = (int)((int64_t)(rank + 1) * num_kt / split);
+  constexpr uint32_t kCols = TP < 32 ? 32 : TP;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    mbar_init(acc_full, 1);
+    mbar_init(drain, 1);
+    *s_abort = 0;
+    fence_mbarrier_init();
+    prefetch_tensormap(&tm_w);
+    prefetch_tensormap(&tm_x);
+  }
+  if (warp == 1) {
+    tmem_alloc(s_tmem, kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *s_tmem;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  bool done = true;   // epilogue warps: the accumulator was there
+  if (warp == 0 && lane == 0) {
+    int g = 0;
+    bool ok = true;
+    for (int kt = kb; kt < ke; ++kt, ++g) {
+      const int s = g % stages;
+      if (!(ok = mbar_wait_bounded(&empty[s], ((uint32_t)(g / stages) & 1u) ^ 1u, wait_budget, s_abort))) break;
+      uint8_t *st = smem + s * G::kStageBytes;
+      mbar_arrive_expect_tx(&full[s], G::kStageBytes);
+      tma_load_2d(st, &tm_w, &full[s], kt * 128, f0);
+      tma_load_2d(st + G::kSmemW, &tm_x, &full[s], kt * 128, 0);
+    }
+    for (int i = g > stages ? g - stages : 0; i < g; ++i) {   // every copy lands before the block ends
+      volatile int no_abort = 0;
+      mbar_wait_bounded(&full[i % stages], (uint32_t)(i / stages) & 1u, kDrainBudget, &no_abort);
+    }
+  } else if (warp == 1 && lane == 0) {
+    constexpr uint32_t idesc = make_idesc_i8(128, TP);
+    const uint64_t a_desc0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+    const uint64_t b_desc0 = smem_desc(smem_u32(smem + G::kSmemW), 16, 1024, kSwizzle128B);
+    int g = 0;
+    bool ok = true;
+    for (int kt = kb; kt < ke; ++kt, ++g) {
+      const int s = g % stages;
+      if (!(ok = mbar_wait_bounded(&full[s], (uint32_t)(g / stages) & 1u, wait_budget, s_abort))) break;
+      tc_fence_after();
+      const uint64_t so = (uint64_t)((s * G::kStageBytes) >> 4);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)   // 32 bytes along the 128-byte swizzled rows each
+        tc_mma_i8(tmem_base, a_desc0 + so + 2 * kk, b_desc0 + so + 2 * kk, idesc, (kt != kb || kk != 0) ? 1u : 0u);
+      tc_commit(&empty[s]);
+    }
+    if (ok) tc_commit(acc_full);
+    else {
+      tc_commit(drain);
+      volatile int no_abort = 0;
+      mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
+    }
+  } else if (warp >= 2) {
+    const int q = warp & 3, f = 32 * q + lane;   // this lane's feature of the tile
+    const float w = f0 + f < N ? __ldg(sw + f0 + f) : 0.0f;
+    auto put = [&](int t, int acc) {
+      const float v = (__int2float_rn(acc) * w) * __ldg(sx + t);
+      const float2 y = GELU ? gelu2(make_float2(v, v)) : make_float2(v, v);
+      Y[(int64_t)t * N + f0 + f] = (uint16_t)f32_to_bits<BF16>(y.x);
+    };
+    const bool got = mbar_wait_bounded(acc_full, 0, wait_budget, s_abort);
+    done = __all_sync(0xFFFFFFFFu, got);
+    if (done) {
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < T; c += 16) {
+        uint32_t r[16];
+        tmem_ld_32x32b_x16(tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)c, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));   // uses stay below the wait
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (split > 1) part[(c + i) * 128 + f] = (int)r[i];
+          else if (c + i < T && f0 + f < N) put(c + i, (int)r[i]);
+        }
+      }
+    }
+    tc_fence_before();
+    if (split > 1) {
+      cluster_sync();   // every CTA's sums are in its shared memory
+      if (done && f0 + f < N) {
+#pragma unroll 1
+        for (int t = rank; t < T; t += split) {
+          const uint32_t at = smem_u32(part + t * 128 + f);
+          int sum = 0;
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (c < split) sum += ld_cluster_s32(at, (uint32_t)c);
+          put(t, sum);
+        }
+      }
+    }
+  }
+  if (split > 1) {
+    if (warp < 2) {
+      __syncwarp();
+      cluster_sync();
+    }
+    __syncwarp();
+    cluster_sync();   // no CTA leaves while its sums are read
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kCols);
+  }
+}
+
+// ------------------------------------------------------------------ one to four tokens
+// Bound by reading Wq once, and by latency: no tensor memory, no barriers, no tensor maps to
+// encode on the host.  A block takes four features; a thread takes every 128th 16-byte unit of
+// K for all four and TT tokens (dp4a, exact), so each unit of Xq serves four rows of Wq.
+constexpr int kI8vThreads = 128;
+constexpr int kI8vRows = 4;
+
+template <int TT, bool BF16, bool GELU>
+__global__ void __launch_bounds__(kI8vThreads)
+    gemv_i8_kernel(const int8_t *__restrict__ Xq, const float *__restrict__ sx, int T, int K,
+                   const int8_t *__restrict__ Wq, const float *__restrict__ sw, int N, uint16_t *__restrict__ Y) {
+  __shared__ int s_sum[kI8vThreads / 32][kI8vRows * TT];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int n0 = blockIdx.x * kI8vRows;
+  const int4 *w = reinterpret_cast<const int4 *>(Wq + (int64_t)n0 * K);
+  const int4 *x = reinterpret_cast<const int4 *>(Xq);
+  const int units = K >> 4;
+  int acc[kI8vRows][TT] = {};
+#pragma unroll 4
+  for (int u = threadIdx.x; u < units; u += kI8vThreads) {
+    int4 wv[kI8vRows], xv[TT];
+#pragma unroll
+    for (int r = 0; r < kI8vRows; ++r) wv[r] = __ldcs(w + (int64_t)r * units + u);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) xv[t] = __ldg(x + (int64_t)min(t, T - 1) * units + u);
+#pragma unroll
+    for (int r = 0; r < kI8vRows; ++r)
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+        acc[r][t] = __dp4a(wv[r].x, xv[t].x, __dp4a(wv[r].y, xv[t].y, __dp4a(wv[r].z, xv[t].z, __dp4a(wv[r].w, xv[t].w, acc[r][t]))));
+  }
+#pragma unroll
+  for (int r = 0; r < kI8vRows; ++r)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const int v = __reduce_add_sync(0xFFFFFFFFu, acc[r][t]);
+      if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5][kI8vRows * t + r] = v;
+    }
+  __syncthreads();
+  const int t = threadIdx.x / kI8vRows, n = n0 + threadIdx.x % kI8vRows;
+  if (t < T && t < TT) {
+    int v = 0;
+#pragma unroll
+    for (int i = 0; i < kI8vThreads / 32; ++i) v += s_sum[i][threadIdx.x];
+    const float y = (__int2float_rn(v) * __ldg(sw + n)) * __ldg(sx + t);
+    Y[(int64_t)t * N + n] = (uint16_t)f32_to_bits<BF16>(GELU ? gelu2(make_float2(y, y)).x : y);
+  }
+}
+
 }  // namespace sp24

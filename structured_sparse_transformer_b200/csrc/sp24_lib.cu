@@ -648,13 +648,13 @@ struct OrthOut {
 };
 
 // Parts that a tail of r tiles of kt K stages on P pairs is split into: the least of the
-// measured times of a tile's main loop (0.38 us a stage), of its epilogue (2.8 us, shared by
-// the parts) and, for s > 1, of the exchange (1.5 us to wait, 5.2 us (s-1)/s to write and add).
+// measured times of a tile's main loop (0.38 us a stage) and, for s > 1, of the exchange (4 us,
+// and 0.4 us for each further part).
 int orth_split(int64_t r, int64_t kt, int64_t P) {
   int best = 1;
-  double least = 0.38 * (double)kt + 2.8;
+  double least = 0.38 * (double)kt;
   for (int64_t s = 2; s <= kOgMaxSplit && s <= kt && r * s <= P; ++s) {
-    const double t = 0.38 * (double)((kt + s - 1) / s) + 2.8 / (double)s + 1.5 + 5.2 * (double)(s - 1) / (double)s;
+    const double t = 0.38 * (double)((kt + s - 1) / s) + 4.0 + 0.4 * (double)(s - 2);
     if (t < least) {
       least = t;
       best = (int)s;
@@ -831,9 +831,67 @@ sp24_status launch_i8_pair(const int8_t *Xq, int64_t T, int64_t K, const int8_t 
                     (int)((K + 127) / 128), (uint64_t)g_wait_budget.load(), sw, sx);
 }
 
+template <int TP, bool BF16, bool GELU>
+sp24_status launch_i8_few(const int8_t *Xq, int64_t T, int64_t K, const int8_t *Wq, int64_t N, void *Y, const float *sx,
+                          const float *sw, cudaStream_t s) {
+  using G = I8sGeom<TP>;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  CUtensorMap tw, tx;
+  if (!make_map_2d(&tw, Wq, (uint64_t)K, (uint64_t)N, (uint64_t)K, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B, u8) ||
+      !make_map_2d(&tx, Xq, (uint64_t)K, (uint64_t)T, (uint64_t)K, 128, TP, CU_TENSOR_MAP_SWIZZLE_128B, u8))
+    return SP24_ERR_CUDA;
+  constexpr auto kernel = gemm_i8_few_kernel<TP, BF16, GELU>;
+  static PerDevice opt_in;   // 1: shared memory granted
+  const int dev = current_device();
+  if (dev < 0) return SP24_ERR_NO_DEVICE;
+  std::call_once(opt_in.once[dev], [&] {
+    opt_in.value[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             G::smem_for(G::kStagesMost)) == cudaSuccess;
+    if (!opt_in.value[dev]) cudaGetLastError();
+  });
+  if (!opt_in.value[dev]) return SP24_ERR_CUDA;
+  // Parts of K: doubled while the CTAs stay within one per SM and each keeps two stages.
+  const int64_t ft = (N + 127) / 128, kt = (K + 127) / 128;
+  int split = 1;
+  while (split < 8 && ft * split * 2 <= sm_count() && kt >= 4 * split) split *= 2;
+  const int64_t mine = (kt + split - 1) / split;
+  const int stages = (int)(mine < G::kStagesMost ? mine : G::kStagesMost);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(ft * split));
+  cfg.blockDim = dim3(kI8sThreads);
+  cfg.dynamicSmemBytes = G::smem_for(stages);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kernel, tw, tx, (int)N, (int)T, (int)kt, split, stages, (uint64_t)g_wait_budget.load(), sw,
+                         sx, static_cast<uint16_t *>(Y)) != cudaSuccess) {
+    cudaGetLastError();
+    return SP24_ERR_CUDA;
+  }
+  return SP24_OK;
+}
+
 template <bool BF16, bool GELU>
 sp24_status launch_i8(const int8_t *Xq, int64_t T, int64_t K, const int8_t *Wq, int64_t N, void *Y, const float *sx,
                       const float *sw, cudaStream_t s) {
+  if (T <= 4) {
+    const dim3 grid((unsigned)(N / kI8vRows));
+    uint16_t *y = static_cast<uint16_t *>(Y);
+    return T == 1   ? launch_pdl(gemv_i8_kernel<1, BF16, GELU>, grid, dim3(kI8vThreads), 0, s, Xq, sx, (int)T, (int)K, Wq, sw, (int)N, y)
+           : T == 2 ? launch_pdl(gemv_i8_kernel<2, BF16, GELU>, grid, dim3(kI8vThreads), 0, s, Xq, sx, (int)T, (int)K, Wq, sw, (int)N, y)
+                    : launch_pdl(gemv_i8_kernel<4, BF16, GELU>, grid, dim3(kI8vThreads), 0, s, Xq, sx, (int)T, (int)K, Wq, sw, (int)N, y);
+  }
+  if (T <= 16) return launch_i8_few<16, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);
+  if (T <= 32) return launch_i8_few<32, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);
+  if (T <= 64) return launch_i8_few<64, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);
+  if (T <= 128) return launch_i8_few<128, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);
   if (((N + 255) / 256) * ((T + 255) / 256) >= sm_count() / 2)
     return launch_i8_pair<256, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);
   return launch_i8_pair<128, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);

@@ -61,7 +61,7 @@ def _check(xq, sx, wq, sw, dtype, epi, stream=None):
     return y
 
 
-SIZES = [(1, 16, 16), (1, 64, 256), (1, 1600, 6400), (2, 48, 80), (3, 5120, 1280), (8, 272, 528), (16, 2064, 400),
+SIZES = [(1, 16, 16), (1, 64, 256), (1, 1600, 6400), (2, 48, 80), (3, 5120, 1280), (4, 1024, 4096), (5, 656, 144), (8, 272, 528), (16, 2064, 400),
          (17, 128, 256), (31, 1600, 112), (32, 6400, 1600), (33, 144, 272), (37, 5120, 1280), (64, 256, 256), (65, 400, 272),
          (100, 96, 1040), (128, 1024, 4096), (129, 1040, 512), (255, 208, 304), (257, 512, 256), (700, 1024, 4096),
          (2047, 1024, 4096), (4096, 640, 2576)]
@@ -79,7 +79,7 @@ def test_product_other_types(T, dtype, epi):
     _check(*_operands(T, 1600, 272, T), dtype, epi)
 
 
-@pytest.mark.parametrize("T", [1, 20, 200])
+@pytest.mark.parametrize("T", [1, 4, 20, 200])
 def test_the_largest_sums_are_exact(T):
     """K at its limit with every product 128 * 128: 2^31 - 2^18 + ..., no overflow and no rounding of the sum."""
     K, N = 131056, 32
@@ -104,7 +104,7 @@ def test_each_operand_entry_lands_where_it_should():
         _check(xq, torch.ones(T), wq, torch.full((N,), 2.0**-8), "f16", None)
 
 
-@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("T", [1, 3, 40])
 def test_scales_of_zero_and_nan(T):
     xq, sx, wq, sw = _operands(T, 320, 64, 9)
     sw[3] = 0.0
@@ -115,7 +115,7 @@ def test_scales_of_zero_and_nan(T):
     assert torch.isnan(y[0]).all() and not torch.isnan(y[1:]).any() and (y[1:, 3] == 0).all()
 
 
-@pytest.mark.parametrize("T", [1, 37, 600])
+@pytest.mark.parametrize("T", [1, 3, 37, 600])
 def test_results_do_not_depend_on_the_batch_and_repeat(T):
     xq, sx, wq, sw = [t.cuda() for t in _operands(T, 1600, 528, 11)]
     outs = []
