@@ -54,7 +54,7 @@ constexpr int kOgChunks = 4;                           // 32-column chunks of a 
 constexpr int kOgStagingBytes = kOgChunks * kOgTileBytes;   // per epilogue warp
 constexpr int kOgStages = 5;
 constexpr int kOgSmem = kOgStages * kOgStageBytes + kOgEpiWarps * kOgStagingBytes + kOgBarBytes + 1024;
-constexpr int kOgMaxSplit = 4;                         // parts of a split tile: a warp has four chunks to share
+constexpr int kOgMaxSplit = 4;                         // parts of a split tile (chunk kk of n belongs to part kk parts / n)
 constexpr int kOgMaxPairs = 80;
 constexpr int kOgMaxSteps = 16;
 // Partial sums of one CTA of a split tile: per epilogue warp and chunk, the registers of its
@@ -72,14 +72,17 @@ static_assert(kOgSmem <= 232448 && 8 * (2 * kOgStages + 7 + kOgEpiWarps) <= kOgB
               "shared memory per CTA");
 
 struct OrthMaps {
-  CUtensorMap x_rows[2], x_cols[2], x_st[2], g_rows, g_st, p_rows, p_st;
+  // Boxes of 64 columns x 128 rows (rows) or 64 rows (half: a K-major operand of narrow tiles,
+  // or X MN-major); st: 32 x 32 store tiles.
+  CUtensorMap x_rows[2], x_half[2], x_st[2], g_rows, g_half, g_st, p_rows, p_st;
 };
 
 struct OrthProducts {
   int m, n;                  // short and long side
   int batch, phases;
-  int sym_tiles, tiles;      // tiles of the symmetric products and of P X, per matrix
-  int split[3];              // parts of a tail tile, by kind
+  int bn[3];                 // by kind: columns of a tile (256 or 128),
+  int tiles[3];              //   tiles per matrix,
+  int split[3];              //   parts of a tail tile
   uint64_t wait_budget;
   float gram_alpha;          // 1 / s^2
   float a, b, c;
@@ -88,34 +91,41 @@ struct OrthProducts {
 };
 
 struct OrthPhase {
-  int kind, in, num_kt, tiles, split;
+  int kind, in, num_kt, bn, tiles, split;
   __device__ OrthPhase(const OrthProducts &p, int ph) {
     kind = ph % 3;
     in = (ph / 3) & 1;
     num_kt = ((kind == kOrthGram ? p.n : p.m) + 63) >> 6;
-    tiles = p.batch * (kind == kOrthApply ? p.tiles : p.sym_tiles);
+    bn = p.bn[kind];
+    tiles = p.batch * p.tiles[kind];
     split = p.split[kind];
   }
 };
 
-// Matrix, first row and first column of a tile; `below`: strictly below the diagonal.
-__device__ __forceinline__ void orth_tile(const OrthProducts &p, int kind, int t, int &b, int &m0, int &n0, bool &below) {
-  if (kind != kOrthApply) {   // row block i has column blocks 0..i
-    b = t / p.sym_tiles;
-    t -= b * p.sym_tiles;
-    int i = (int)((sqrtf(1.0f + 8.0f * (float)t) - 1.0f) * 0.5f);
-    while (i * (i + 1) / 2 > t) --i;
-    while ((i + 1) * (i + 2) / 2 <= t) ++i;
-    const int j = t - i * (i + 1) / 2;
+// Tiles of a symmetric product: rows in blocks of 256, columns in blocks of bn (R = 256/bn per
+// row block); row block i has column blocks 0 .. R(i+1)-1, cut at the matrix's edge.
+__host__ __device__ constexpr int64_t orth_sym_tiles(int64_t m, int bn) {
+  const int64_t rb = (m + 255) / 256, r = 256 / bn, cb = (m + bn - 1) / bn;
+  return r * rb * (rb - 1) / 2 + (cb < r * rb ? cb : r * rb);
+}
+
+// Matrix, first row and first column of a tile; `below`: strictly below the diagonal blocks.
+__device__ __forceinline__ void orth_tile(const OrthProducts &p, const OrthPhase &f, int t, int &b, int &m0, int &n0,
+                                          bool &below) {
+  b = t / p.tiles[f.kind];
+  t -= b * p.tiles[f.kind];
+  if (f.kind != kOrthApply) {
+    const int R = 256 / f.bn;
+    int i = (int)((sqrtf(1.0f + 8.0f * (float)t / (float)R) - 1.0f) * 0.5f);
+    while (R * i * (i + 1) / 2 > t) --i;
+    while (R * (i + 1) * (i + 2) / 2 <= t) ++i;
     m0 = i * 256;
-    n0 = j * 256;
-    below = j < i;
+    n0 = (t - R * i * (i + 1) / 2) * f.bn;
+    below = n0 < m0;
   } else {
-    b = t / p.tiles;
-    t -= b * p.tiles;
     const int num_mt = (p.m + 255) / 256;
     m0 = (t % num_mt) * 256;
-    n0 = (t / num_mt) * 256;
+    n0 = (t / num_mt) * f.bn;
     below = false;
   }
 }
@@ -186,10 +196,10 @@ __device__ __forceinline__ void regs_fence(uint32_t (&r)[16]) {
 
 // Passes on a warp's chunks that other parts finish.  Not inlined: inlined, the compiler keeps
 // its registers beside the epilogue's and spills.
-__device__ __noinline__ void orth_pass_chunks(uint32_t taddr, int nch, int part, int parts, float4 *slot) {
+__device__ __noinline__ void orth_pass_chunks(uint32_t taddr, int nch, int halves, int part, int parts, float4 *slot) {
 #pragma unroll 1
   for (int kk = 0; kk < nch; ++kk) {
-    if (((kk * parts) >> 2) == part) continue;
+    if (((kk * parts) >> halves) == part) continue;
     uint32_t r[2][16];
     tmem_ld_16x256b_x4(taddr + (uint32_t)(32 * kk), r[0]);
     tmem_ld_16x256b_x4(taddr + (uint32_t)(32 * kk) + (16u << 16), r[1]);
@@ -282,12 +292,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
         const CUtensorMap *ma, *mb;
         const bool b_mn = f.kind == kOrthApply;
         if (f.kind == kOrthGram) {
-          ma = mb = &maps.x_rows[f.in];
+          ma = &maps.x_rows[f.in];
+          mb = f.bn == 256 ? ma : &maps.x_half[f.in];
         } else if (f.kind == kOrthPoly) {
-          ma = mb = &maps.g_rows;
+          ma = &maps.g_rows;
+          mb = f.bn == 256 ? ma : &maps.g_half;
         } else {
           ma = &maps.p_rows;
-          mb = &maps.x_cols[f.in];
+          mb = &maps.x_half[f.in];
         }
         prefetch_tensormap(ma);
         prefetch_tensormap(mb);
@@ -298,8 +310,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
         while (ok && sched.next(tile, kb, ke)) {
           int b, m0, n0;
           bool below;
-          orth_tile(p, f.kind, tile, b, m0, n0, below);
-          const int a_row = m0 + (int)rank * 128, b_row = n0 + (int)rank * 128;
+          orth_tile(p, f, tile, b, m0, n0, below);
+          const int a_row = m0 + (int)rank * 128, b_row = n0 + (int)rank * (f.bn / 2);
           for (int kt = kb; kt < ke; ++kt, ++g) {
             const int s = (int)(g % kStages);
             if (!mbar_wait_bounded(&empty[s], ((g / kStages) & 1u) ^ 1u, p.wait_budget, s_abort)) {
@@ -307,12 +319,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
               break;
             }
             uint8_t *st = smem + s * kOgStageBytes;
-            if (is_leader) mbar_arrive_expect_tx(&full[s], 2 * kOgStageBytes);
-            // K-major: 128 rows of 64 entries along K; MN-major: two 64-column atoms of 64 rows.
+            if (is_leader) mbar_arrive_expect_tx(&full[s], 2 * (16384 + 64 * f.bn));
+            // K-major: rows of 64 entries along K; MN-major: two 64-column atoms of 64 rows.
             tma_load_3d_pair(st, ma, &full[s], kt * 64, a_row, b);
             if (b_mn) {
               tma_load_3d_pair(st + 16384, mb, &full[s], b_row, kt * 64, b);
-              tma_load_3d_pair(st + 24576, mb, &full[s], b_row + 64, kt * 64, b);
+              if (f.bn == 256) tma_load_3d_pair(st + 24576, mb, &full[s], b_row + 64, kt * 64, b);
             } else {
               tma_load_3d_pair(st + 16384, mb, &full[s], kt * 64, b_row, b);
             }
@@ -336,7 +348,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
     for (int ph = 0; ok && ph < p.phases; ++ph) {
       const OrthPhase f(p, ph);
       const bool b_mn = f.kind == kOrthApply;
-      const uint32_t idesc = make_idesc_dense(false, 256, 256) | (b_mn ? 1u << 16 : 0u);
+      const uint32_t idesc = make_idesc_dense(false, 256, f.bn) | (b_mn ? 1u << 16 : 0u);
       const uint64_t a_desc0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
       const uint64_t b_desc0 = smem_desc(smem_u32(smem + 16384), b_mn ? 8192 : 16, 1024, kSwizzle128B);
       // A K step of 16 moves 32 bytes along the rows, or 16 rows of 128 bytes.
@@ -369,10 +381,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
     }
   } else if (warp >= 2) {
     // ---------------------------------------------------- epilogue (both CTAs)
-    // Warp w drains lanes 32q..32q+31 (q = w%4) at columns 128 grp .. 128 grp + 127, four chunks
-    // of 32.  Gram, Poly and Apply: register 16h + 4i + 2 sub + e of chunk kk, lane l, is row
-    // 16h + 8 sub + l/4, column 8i + 2(l%4) + e of the chunk.  Last: register i is column i
-    // of row l.
+    // Warp w drains lanes 32q..32q+31 (q = w%4) at its half (grp) of the columns, four or two chunks
+    // of 32, two at a time: register 4i + 2 sub + e of [chunk][h], lane l, is row 16h + 8 sub +
+    // l/4, column 8i + 2(l%4) + e of the chunk.
     const int ew = warp - 2, grp = ew >> 2, q = warp & 3;
     uint8_t *stg = epi_smem + ew * kOgStagingBytes;
     const uint32_t stg_u32 = smem_u32(stg);
@@ -399,14 +410,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
       for (; alive && sched.next(tile, kb, ke); ++j) {
         int b, m0, n0;
         bool below;
-        orth_tile(p, f.kind, tile, b, m0, n0, below);
+        orth_tile(p, f, tile, b, m0, n0, below);
         m0 += (int)rank * 128 + 32 * q;
-        n0 += 128 * grp;
+        n0 += f.bn / 2 * grp;
+        const int halves = f.bn / 128;                        // pairs of chunks of this warp
         const bool split = ke - kb < f.num_kt;
         const int part = split ? pair % f.split : 0, parts = split ? f.split : 1;
-        const int nch = min(kOgChunks, (N - n0 + 31) >> 5);   // chunks inside the matrix (none: <= 0)
+        const int nch = min(2 * halves, (N - n0 + 31) >> 5);  // chunks inside the matrix (none: <= 0)
         const int buf = j & 1;
-        auto mine = [&](int kk) { return kk < nch && ((kk * parts) >> 2) == part; };   // chunks that this part finishes
+        auto mine = [&](int kk) { return kk < nch && ((kk * parts) >> halves) == part; };   // chunks that this part finishes
         // The other parts have passed on this warp's chunks: one lane waits for each.
         auto others_ready = [&]() {
           bool ready_flag = true;
@@ -425,7 +437,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_leader(&acc_empty[buf]);
         };
-        const uint32_t t_base = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * 256 + 128 * grp);
+        const uint32_t t_base = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * 256 + f.bn / 2 * grp);
 
         // Poly: G's entries of the warp's chunks, by TMA into its staging tiles, once the phase
         // before is written (the producer acquired it for the CTA).
@@ -456,7 +468,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
         }
         tc_fence_after();
         if (split) {
-          orth_pass_chunks(t_base, nch, part, parts, part_own);
+          orth_pass_chunks(t_base, nch, halves, part, parts, part_own);
           flag_passed();
           if (!others_ready()) {
             alive = false;
@@ -480,10 +492,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
         }
         const float alpha = f.kind == kOrthGram ? p.gram_alpha : 1.0f;
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
+        for (int half = 0; half < halves; ++half) {
           uint32_t r[2][2][16];
           orth_load_half(t_base + (uint32_t)(64 * half), nch - 2 * half, r);
-          if (half == 1) release_acc();
+          if (half == halves - 1) release_acc();
           if (!mine(2 * half) && !mine(2 * half + 1)) continue;
           if (split) {   // add the other parts' sums to its own, in part order
 #pragma unroll 1

@@ -594,7 +594,7 @@ int pairs_of() {
 // (fp16), and the split tiles' partial sums.
 struct OrthPlan {
   int64_t count, rows, cols, m, n, ldx, ldm;
-  int64_t sym_tiles, tiles;                 // 256 x 256 tiles of the symmetric products and of P X, per matrix
+  int64_t tiles;                            // 256 x 256 tiles of P X, per matrix
   size_t counters, norm, x0, x1, gram, poly, part, total;   // byte offsets
   bool tall;
 };
@@ -620,11 +620,11 @@ sp24_status orth_plan(int64_t count, int64_t rows, int64_t cols, OrthPlan *p) {
   };
   const size_t bx = (size_t)count * p->m * p->ldx * 2, bm = (size_t)count * p->m * p->ldm * 2;
   const int64_t mb = (p->m + 255) / 256, nb = (p->n + 255) / 256;
-  p->sym_tiles = mb * (mb + 1) / 2;
   p->tiles = mb * nb;
-  if (count * (p->sym_tiles > p->tiles ? p->sym_tiles : p->tiles) > INT32_MAX) return SP24_ERR_UNSUPPORTED_SHAPE;
-  // A launch has at most kOgMaxSplit pairs per tile, and at most kOgMaxPairs.
-  const int64_t want = kOgMaxSplit * count * p->tiles;
+  if (2 * count * p->tiles > INT32_MAX) return SP24_ERR_UNSUPPORTED_SHAPE;
+  // A launch has at most kOgMaxSplit pairs per tile (of 128 columns, twice as many), and at
+  // most kOgMaxPairs.
+  const int64_t want = kOgMaxSplit * 2 * count * p->tiles;
   const int64_t slots = want < kOgMaxPairs ? want : kOgMaxPairs;
   p->counters = take(kOgCounters * sizeof(unsigned));
   p->norm = take((size_t)count * kOrthMaxBlocks * sizeof(double));
@@ -647,36 +647,67 @@ struct OrthOut {
   bool bf16;
 };
 
-// Parts that a tail of r tiles of kt K stages on P pairs is split into: the least of the
-// measured times of a tile's main loop (0.38 us a stage) and, for s > 1, of the exchange (4 us,
-// and 0.4 us for each further part).
-int orth_split(int64_t r, int64_t kt, int64_t P) {
-  int best = 1;
-  double least = 0.38 * (double)kt;
-  for (int64_t s = 2; s <= kOgMaxSplit && s <= kt && r * s <= P; ++s) {
-    const double t = 0.38 * (double)((kt + s - 1) / s) + 4.0 + 0.4 * (double)(s - 2);
-    if (t < least) {
-      least = t;
-      best = (int)s;
+// Width of a phase's tiles and parts of its tail, by the least time in microseconds, from
+// phases of the FFN-sized and small cases measured alone: a K stage of a tile of 256 columns
+// (0.31 alone, 0.38 beside all other pairs, 0.45 with X read MN-major) and of 128 columns (0.25
+// to 0.35: bound by shared memory, so more than half), a tile's epilogue, and the exchange of
+// a split tile.  At 777 x 1333 narrow tiles take 9 us for P X where wide ones took 13; at
+// 1600 x 6400 they take 40 where wide ones take 32.
+struct OrthShape {
+  int bn, split;
+  int64_t use;      // pairs with work
+  double us;
+};
+
+double orth_stage_us(int bn, bool apply, int64_t use, int64_t P) {
+  const double share = (double)use / (double)P;
+  return bn == 128 ? 0.25 + 0.10 * share : 0.31 + (apply ? 0.14 : 0.07) * share;
+}
+
+OrthShape orth_shape(int64_t tiles, int64_t kt, int64_t P, int bn, bool apply) {
+  OrthShape o = {bn, 1, tiles < P ? tiles : P, 0.0};
+  o.us = orth_stage_us(bn, apply, P, P) * (double)(tiles / P * kt) + (bn == 256 ? 2.4 : 1.4);
+  const int64_t tail = tiles % P;
+  if (tail) {
+    double least = orth_stage_us(bn, apply, tail, P) * (double)kt;
+    for (int64_t s = 2; s <= kOgMaxSplit && s <= kt && tail * s <= P; ++s) {
+      const double t = orth_stage_us(bn, apply, tail * s, P) * (double)((kt + s - 1) / s) + (bn == 256 ? 3.5 : 2.8) +
+                       0.4 * (double)(s - 2);
+      if (t < least) {
+        least = t;
+        o.split = (int)s;
+      }
     }
+    o.us += least;
+    if (tiles < P) o.use = tail * o.split;
   }
-  return best;
+  return o;
 }
 
 sp24_status launch_orth_products(const OrthMaps &maps, OrthProducts p, cudaStream_t stream) {
   int64_t P = pairs_of<orth_products_kernel, kOgThreads, kOgSmem>();
   if (P <= 0) return P == 0 ? SP24_ERR_CUDA : SP24_ERR_NO_DEVICE;
   if (P > kOgMaxPairs) P = kOgMaxPairs;
-  const int64_t all[3] = {(int64_t)p.batch * p.sym_tiles, (int64_t)p.batch * p.sym_tiles, (int64_t)p.batch * p.tiles};
-  const int64_t kt[3] = {(p.n + 63) / 64, (p.m + 63) / 64, (p.m + 63) / 64};
+  const int64_t mb = (p.m + 255) / 256;
   int64_t grid = 0;   // pairs: as many as the phase that uses most
   for (int k = 0; k < 3; ++k) {
-    const int64_t use = all[k] >= P ? P : all[k] * orth_split(all[k], kt[k], P);
-    if (use > grid) grid = use;
+    const bool apply = k == kOrthApply;
+    const int64_t kt = ((k == kOrthGram ? p.n : p.m) + 63) / 64;
+    OrthShape best = {};
+    for (int bn = 128; bn <= 256; bn += 128) {
+      const int64_t per = apply ? mb * (((int64_t)p.n + bn - 1) / bn) : orth_sym_tiles(p.m, bn);
+      const OrthShape o = orth_shape(p.batch * per, kt, P, bn, apply);
+      if (best.bn == 0 || o.us <= best.us) {
+        best = o;
+        p.tiles[k] = (int)per;
+      }
+    }
+    p.bn[k] = best.bn;
+    if (best.use > grid) grid = best.use;
   }
-  for (int k = 0; k < 3; ++k) {
-    const int64_t tail = all[k] % grid;
-    p.split[k] = tail ? orth_split(tail, kt[k], grid) : 1;
+  for (int k = 0; k < 3; ++k) {   // the splits on that many pairs
+    const int64_t kt = ((k == kOrthGram ? p.n : p.m) + 63) / 64;
+    p.split[k] = orth_shape((int64_t)p.batch * p.tiles[k], kt, grid, p.bn[k], k == kOrthApply).split;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * (unsigned)grid);
@@ -722,14 +753,14 @@ sp24_status run_orth(const OrthPlan &pl, OrthSrc src, const OrthOut &o, int step
   const uint64_t px = (uint64_t)pl.ldx * 2, pm = (uint64_t)pl.ldm * 2;
   const uint64_t m = (uint64_t)pl.m, n = (uint64_t)pl.n, bt = (uint64_t)pl.count;
   const CUtensorMapSwizzle s128 = CU_TENSOR_MAP_SWIZZLE_128B, s64 = CU_TENSOR_MAP_SWIZZLE_64B;
-  // rows: a K-major operand; cols: the MN-major one; st: 32 x 32 store tiles.
   OrthMaps maps;
   bool ok = true;
   for (int i = 0; i < 2; ++i)
     ok = ok && make_map_3d(&maps.x_rows[i], xb[i], n, m, bt, px, m * px, 64, 128, s128) &&
-         make_map_3d(&maps.x_cols[i], xb[i], n, m, bt, px, m * px, 64, 64, s128) &&
+         make_map_3d(&maps.x_half[i], xb[i], n, m, bt, px, m * px, 64, 64, s128) &&
          make_map_3d(&maps.x_st[i], xb[i], n, m, bt, px, m * px, 32, 32, s64);
   ok = ok && make_map_3d(&maps.g_rows, gram, m, m, bt, pm, m * pm, 64, 128, s128) &&
+       make_map_3d(&maps.g_half, gram, m, m, bt, pm, m * pm, 64, 64, s128) &&
        make_map_3d(&maps.g_st, gram, m, m, bt, pm, m * pm, 32, 32, s64) &&
        make_map_3d(&maps.p_rows, poly, m, m, bt, pm, m * pm, 64, 128, s128) &&
        make_map_3d(&maps.p_st, poly, m, m, bt, pm, m * pm, 32, 32, s64);
@@ -769,8 +800,6 @@ sp24_status run_orth(const OrthPlan &pl, OrthSrc src, const OrthOut &o, int step
   p.n = (int)pl.n;
   p.batch = (int)pl.count;
   p.phases = 3 * steps - 1;
-  p.sym_tiles = (int)pl.sym_tiles;
-  p.tiles = (int)pl.tiles;
   p.wait_budget = g_wait_budget.load();
   p.gram_alpha = 1.0f / (s * s);
   p.a = kNsA;
@@ -790,7 +819,7 @@ sp24_status run_orth(const OrthPlan &pl, OrthSrc src, const OrthOut &o, int step
   l.keep = o.keep;
   l.w = o.w;
   l.out16 = o.out16;
-  const CUtensorMap &x_cols = maps.x_cols[(steps - 1) & 1];
+  const CUtensorMap &x_cols = maps.x_half[(steps - 1) & 1];
   if (o.bf16)
     return o.w ? launch_orth_last<true, true>(maps.p_rows, x_cols, pl.tall, l, stream)
                : launch_orth_last<true, false>(maps.p_rows, x_cols, pl.tall, l, stream);

@@ -169,7 +169,7 @@ def test_valid_calls_without_a_device_report_no_device():
 def test_tile_numbering_of_the_symmetric_products():
     """Every block on and below the diagonal once, none above: the kernel's numbering restated."""
     for m in (1, 100, 128, 129, 256, 257, 700, 1600, 5000):
-        for bn in (256,):
+        for bn in (128, 256):
             R, rb, cb = 256 // bn, -(-m // 256), -(-m // bn)
             total = R * rb * (rb - 1) // 2 + min(cb, R * rb)
             seen = set()
