@@ -85,6 +85,7 @@ struct OrthProducts {
   int split[3];              //   parts of a tail tile
   uint64_t wait_budget;
   float gram_alpha;          // 1 / s^2
+  const float *gamma;        // [batch] round 0: s X0 = gamma X
   float a, b, c;
   float *part;
   unsigned *counters;
@@ -278,39 +279,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------ producer (both CTAs)
-    // Lane w waits for the epilogue warps w of every CTA; lane 0 issues the loads.
+    // Lane w waits for the epilogue warps w of every CTA; lane 0 issues the loads.  What does not
+    // depend on the phase before is done ahead of the wait.
     uint32_t g = 0;
     bool ok = true;
     for (int ph = 0; ok && ph < p.phases; ++ph) {
+      const OrthPhase f(p, ph);
+      const bool b_mn = f.kind == kOrthApply;
+      const CUtensorMap *ma = f.kind == kOrthGram ? &maps.x_rows[f.in] : (f.kind == kOrthPoly ? &maps.g_rows : &maps.p_rows);
+      const CUtensorMap *mb = b_mn ? &maps.x_half[f.in]
+                                   : (f.bn == 256 ? ma : (f.kind == kOrthGram ? &maps.x_half[f.in] : &maps.g_half));
+      if (lane == 0) {
+        prefetch_tensormap(ma);
+        prefetch_tensormap(mb);
+      }
+      PairSchedule sched(f.split, pair, npairs, f.tiles, f.num_kt);
+      int tile, kb, ke, b = 0, m0 = 0, n0 = 0;
+      bool below, more = sched.next(tile, kb, ke);
+      if (more) orth_tile(p, f, tile, b, m0, n0, below);
       bool up = true;
       if (ph > 0 && lane < kOgEpiWarps)   // all of the phase before is written
         up = flag_spin_bounded(p.counters + lane * kOgPhases + ph - 1, gridDim.x, p.wait_budget, s_abort);
       if (!__all_sync(0xFFFFFFFFu, up)) break;
       __syncwarp();
       if (lane == 0) {
-        const OrthPhase f(p, ph);
-        const CUtensorMap *ma, *mb;
-        const bool b_mn = f.kind == kOrthApply;
-        if (f.kind == kOrthGram) {
-          ma = &maps.x_rows[f.in];
-          mb = f.bn == 256 ? ma : &maps.x_half[f.in];
-        } else if (f.kind == kOrthPoly) {
-          ma = &maps.g_rows;
-          mb = f.bn == 256 ? ma : &maps.g_half;
-        } else {
-          ma = &maps.p_rows;
-          mb = &maps.x_half[f.in];
-        }
-        prefetch_tensormap(ma);
-        prefetch_tensormap(mb);
         fence_proxy_async_all();
         mbar_arrive(ready);
-        PairSchedule sched(f.split, pair, npairs, f.tiles, f.num_kt);
-        int tile, kb, ke;
-        while (ok && sched.next(tile, kb, ke)) {
-          int b, m0, n0;
-          bool below;
-          orth_tile(p, f, tile, b, m0, n0, below);
+        while (ok && more) {
           const int a_row = m0 + (int)rank * 128, b_row = n0 + (int)rank * (f.bn / 2);
           for (int kt = kb; kt < ke; ++kt, ++g) {
             const int s = (int)(g % kStages);
@@ -320,7 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
             }
             uint8_t *st = smem + s * kOgStageBytes;
             if (is_leader) mbar_arrive_expect_tx(&full[s], 2 * (16384 + 64 * f.bn));
-            // K-major: rows of 64 entries along K; MN-major: two 64-column atoms of 64 rows.
+            // K-major: rows of 64 entries along K; MN-major: 64-column atoms of 64 rows.
             tma_load_3d_pair(st, ma, &full[s], kt * 64, a_row, b);
             if (b_mn) {
               tma_load_3d_pair(st + 16384, mb, &full[s], b_row, kt * 64, b);
@@ -329,6 +324,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
               tma_load_3d_pair(st + 16384, mb, &full[s], kt * 64, b_row, b);
             }
           }
+          more = sched.next(tile, kb, ke);
+          if (more) orth_tile(p, f, tile, b, m0, n0, below);
         }
       }
       ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
@@ -490,7 +487,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
           if (lane == 0) bulk_wait_group_read<0>();
           __syncwarp();
         }
-        const float alpha = f.kind == kOrthGram ? p.gram_alpha : 1.0f;
+        const float gamma = ph < 3 ? __ldg(p.gamma + b) : 1.0f;
+        const float alpha = f.kind == kOrthGram ? p.gram_alpha * gamma * gamma : gamma;
 #pragma unroll 1
         for (int half = 0; half < halves; ++half) {
           uint32_t r[2][2][16];
@@ -626,6 +624,7 @@ struct OrthLast {
   int batch, tiles;          // tiles per matrix
   uint64_t wait_budget;
   float alpha;               // 1/s, or step/s
+  const float *gamma;        // [batch], with one round: s X0 = gamma X; else null
   float keep;
   float *w;                  // [batch][rows][cols]
   uint16_t *out16;           // [batch][rows][cols]; UPDATE: may be null
@@ -780,6 +779,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOlThreads, 1)
       const int row0 = n0 + 64 * grp;
       const int left = p.rows - row0;   // rows of the matrix from this warp's first on
       const int64_t at = ((int64_t)b * p.rows + row0) * p.cols;
+      const float alpha = p.gamma ? p.alpha * __ldg(p.gamma + b) : p.alpha;
       const float *w_src = p.w + at + min(col, p.cols - 1);   // loads past the last column repeat it
       float pre[32];
       if (UPDATE && left > 0) orth_load_rows(w_src, p.cols, left, pre);
@@ -806,7 +806,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOlThreads, 1)
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const float acc = __uint_as_float(r[i]);
-          r[i] = __float_as_uint(UPDATE ? fmaf(-p.alpha, acc, p.keep * pre[i]) : p.alpha * acc);
+          r[i] = __float_as_uint(UPDATE ? fmaf(-alpha, acc, p.keep * pre[i]) : alpha * acc);
         }
         if (UPDATE && k == 0 && left > 32) orth_load_rows(w_src + (int64_t)32 * p.cols, p.cols, left - 32, pre);
         const int n_rows = col < p.cols ? left - 32 * k : 0;

@@ -595,7 +595,7 @@ int pairs_of() {
 struct OrthPlan {
   int64_t count, rows, cols, m, n, ldx, ldm;
   int64_t tiles;                            // 256 x 256 tiles of P X, per matrix
-  size_t counters, norm, x0, x1, gram, poly, part, total;   // byte offsets
+  size_t counters, norm, gamma, x0, x1, gram, poly, part, total;   // byte offsets
   bool tall;
 };
 
@@ -627,7 +627,8 @@ sp24_status orth_plan(int64_t count, int64_t rows, int64_t cols, OrthPlan *p) {
   const int64_t want = kOgMaxSplit * 2 * count * p->tiles;
   const int64_t slots = want < kOgMaxPairs ? want : kOgMaxPairs;
   p->counters = take(kOgCounters * sizeof(unsigned));
-  p->norm = take((size_t)count * kOrthMaxBlocks * sizeof(double));
+  p->norm = take((size_t)count * kOrthMaxBlocks * sizeof(OrthPart));
+  p->gamma = take((size_t)count * sizeof(float));
   p->x0 = take(bx);
   p->x1 = take(bx);
   p->gram = take(bm);
@@ -747,7 +748,8 @@ sp24_status run_orth(const OrthPlan &pl, OrthSrc src, const OrthOut &o, int step
                      cudaStream_t stream) {
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   unsigned *counters = reinterpret_cast<unsigned *>(ws + pl.counters);
-  double *part = reinterpret_cast<double *>(ws + pl.norm);
+  OrthPart *part = reinterpret_cast<OrthPart *>(ws + pl.norm);
+  float *gamma = reinterpret_cast<float *>(ws + pl.gamma);
   __half *xb[2] = {reinterpret_cast<__half *>(ws + pl.x0), reinterpret_cast<__half *>(ws + pl.x1)};
   void *gram = ws + pl.gram, *poly = ws + pl.poly;
   const uint64_t px = (uint64_t)pl.ldx * 2, pm = (uint64_t)pl.ldm * 2;
@@ -771,28 +773,24 @@ sp24_status run_orth(const OrthPlan &pl, OrthSrc src, const OrthOut &o, int step
   while ((int64_t(1) << (2 * (e + 1))) <= pl.n) ++e;
   const float s = (float)(1 << e);
 
-  const bool vec = src.ld == src.cols && src.stride == src.rows * src.cols && (src.rows * src.cols) % 4 == 0 &&
-                   aligned16(src.g) && (!src.m || aligned16(src.m));
-  const int64_t entries = pl.m * pl.n;
-  int64_t blocks = (entries + 16 * kOrthThreads - 1) / (16 * kOrthThreads);
-  const int64_t cap = 4 * (int64_t)sm_count() / pl.count;
-  if (blocks > cap) blocks = cap < 1 ? 1 : cap;
-  if (blocks > kOrthMaxBlocks) blocks = kOrthMaxBlocks;
-  const dim3 grid1((unsigned)blocks, (unsigned)pl.count);
-  sp24_status st = vec ? launch_pdl(orth_sumsq_kernel<true>, grid1, dim3(kOrthThreads), 0, stream, src, part)
-                       : launch_pdl(orth_sumsq_kernel<false>, grid1, dim3(kOrthThreads), 0, stream, src, part);
-  if (st != SP24_OK) return st;
   const int64_t col_tiles = (pl.cols + kOrthTile - 1) / kOrthTile;
   const int64_t tiles = col_tiles * ((pl.rows + kOrthTile - 1) / kOrthTile);
-  int64_t per = (8 * (int64_t)sm_count() + pl.count - 1) / pl.count;   // eight blocks of 256 threads an SM
-  if (per > tiles) per = tiles;
-  const dim3 grid2((unsigned)per, (unsigned)pl.count);
+  int64_t blocks = (6 * (int64_t)sm_count() + pl.count - 1) / pl.count;   // six blocks of 256 threads an SM
+  if (blocks > tiles) blocks = tiles;
+  if (blocks > kOrthMaxBlocks) blocks = kOrthMaxBlocks;
+  const dim3 grid((unsigned)blocks, (unsigned)pl.count);
   const bool quads = src.cols % 4 == 0 && src.ld % 4 == 0 && src.stride % 4 == 0 && aligned16(src.g) &&
                      (!src.m || aligned16(src.m));
-  auto scale = pl.tall ? (quads ? orth_scale_kernel<true, true> : orth_scale_kernel<true, false>)
-                       : (quads ? orth_scale_kernel<false, true> : orth_scale_kernel<false, false>);
-  st = launch_pdl(scale, grid2, dim3(kOrthThreads), 0, stream, src, part, (int)blocks, s, eps, xb[0], pl.ldx, col_tiles,
-                  tiles, counters, kOgCounters);
+  auto start = pl.tall ? (quads ? orth_start_kernel<true, true> : orth_start_kernel<true, false>)
+                       : (quads ? orth_start_kernel<false, true> : orth_start_kernel<false, false>);
+  sp24_status st = launch_pdl(start, grid, dim3(kOrthThreads), 0, stream, src, part, xb[0], pl.ldx, col_tiles, tiles);
+  if (st != SP24_OK) return st;
+  auto finish = pl.tall ? (quads ? orth_finish_start_kernel<true, true> : orth_finish_start_kernel<true, false>)
+                        : (quads ? orth_finish_start_kernel<false, true> : orth_finish_start_kernel<false, false>);
+  const int64_t few = (2 * (int64_t)sm_count() + pl.count - 1) / pl.count;
+  const dim3 grid2((unsigned)(blocks < few ? blocks : few), (unsigned)pl.count);
+  st = launch_pdl(finish, grid2, dim3(kOrthThreads), 0, stream, src, part, (int)blocks, s, eps, xb[0], pl.ldx, col_tiles,
+                  tiles, gamma, counters, kOgCounters);
   if (st != SP24_OK) return st;
 
   OrthProducts p = {};
@@ -802,6 +800,7 @@ sp24_status run_orth(const OrthPlan &pl, OrthSrc src, const OrthOut &o, int step
   p.phases = 3 * steps - 1;
   p.wait_budget = g_wait_budget.load();
   p.gram_alpha = 1.0f / (s * s);
+  p.gamma = gamma;
   p.a = kNsA;
   p.b = kNsB;
   p.c = kNsC;
@@ -816,6 +815,7 @@ sp24_status run_orth(const OrthPlan &pl, OrthSrc src, const OrthOut &o, int step
   l.tiles = (int)pl.tiles;
   l.wait_budget = p.wait_budget;
   l.alpha = (o.w ? o.step : 1.0f) / s;
+  l.gamma = steps == 1 ? gamma : nullptr;
   l.keep = o.keep;
   l.w = o.w;
   l.out16 = o.out16;

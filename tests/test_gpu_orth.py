@@ -284,3 +284,42 @@ def test_from_the_gradient_to_the_8_bit_layer():
         assert ((y.double() - ref).abs() <= 2.0**-11 * ref.abs() + z.abs() * 1.5e-5 + 2.0**-25 + 4.4e-8).all()
         a = y
     assert sp.sp24_device_status() == 0
+
+
+@pytest.mark.parametrize("shape", [(96, 200), (200, 96), (3, 61, 130)])
+@pytest.mark.parametrize("case", ["zero gradient", "tiny gradient", "momentum of the other sign", "a huge entry",
+                                  "zeros where sizes are guessed"])
+def test_starts_of_unusual_sizes(shape, case):
+    """The first fp16 iterate's power of two is guessed from the gradient at some places; where the guess does not
+    serve, the result is the same."""
+    g, m = _grad(shape, 1), _grad(shape, 2, 5e-3)
+    if case == "zero gradient":
+        g.zero_()
+    elif case == "tiny gradient":
+        g *= 1e-20
+    elif case == "momentum of the other sign":
+        m = -g / 0.95 * (1 + 1e-6)
+    elif case == "a huge entry":
+        g.view(-1)[g.numel() // 3 + 1] = 3e4
+    else:
+        n = shape[-1] * shape[-2]
+        at = (n // 8 * torch.arange(8)[:, None] + torch.arange(32)).flatten().clamp_max(n - 1).cuda()
+        g.view(-1, n)[:, at] = 0.0
+    w = _grad(shape, 3, 0.02)
+    w0 = w.clone()
+    _, u, o, _ = _muon_reference(g, m, w, 0.95, True, 0.05, 0.0, 1.0)
+    sp.sp24_muon_step(g, m, w, None, _workspace(g), lr=0.05)
+    if case == "momentum of the other sign":     # what cancels in U is rounded to 32 bits there: take U's own value
+        u = g.double() + 0.95 * m.double()
+        u = u.float()
+        o = torch.stack([_ns(x) for x in (u if u.dim() == 3 else u[None])]).view(u.shape)
+    u3 = u if u.dim() == 3 else u[None]
+    upd = (w0.double() - w.double()) / 0.05
+    tol = max(_tol(x) for x in u3) + 2.0**-22 * (w0.double().norm() / (0.05 * o.norm())).item()
+    if case == "momentum of the other sign":     # (the fp32 sum of U: half a step of |g| + |mu m|, over |U|; the
+        tol = tol + 3.4445**5 * (2.0**-23 * 2 * g.double().norm() / u.double().norm()).item()   # rounds raise small parts a^5 times)
+    assert _rel(upd, o) <= tol
+    one = torch.empty(*shape, dtype=torch.float16, device="cuda")
+    sp.sp24_orthogonalize(u.float().contiguous(), one, _workspace(g), steps=1)
+    ref = torch.stack([_ns(x.float(), 1) for x in u3]).view(u.shape)
+    assert _rel(one, ref) <= max(_tol(x.float(), torch.float16, 1) for x in u3)
