@@ -13,6 +13,9 @@
 // counter of the phase once its stores are complete, and every TMA producer waits for the
 // counts: only the producers stall, tensor memory, barriers and descriptors stay set up.
 // (As 15 launches, each phase paid for launch, set-up and drain: about 9 us each.)
+// Small matrices (CLUSTER) take a cluster of CTA pairs each instead: they need not wait for one
+// another, no cooperative launch is needed, and the counts become arrivals on an mbarrier of
+// every CTA of the cluster instead of counters in L2.
 //
 // Gram and Poly are symmetric: only tiles on and below the diagonal are computed, and a tile
 // below it is stored a second time, transposed (stmatrix.trans on the same registers), so
@@ -86,6 +89,7 @@ struct OrthProducts {
   uint64_t wait_budget;
   float gram_alpha;          // 1 / s^2
   const float *gamma;        // [batch] round 0: s X0 = gamma X
+  int cluster;               // CLUSTER: CTAs per matrix
   float a, b, c;
   float *part;
   unsigned *counters;
@@ -111,10 +115,11 @@ __host__ __device__ constexpr int64_t orth_sym_tiles(int64_t m, int bn) {
 }
 
 // Matrix, first row and first column of a tile; `below`: strictly below the diagonal blocks.
-__device__ __forceinline__ void orth_tile(const OrthProducts &p, const OrthPhase &f, int t, int &b, int &m0, int &n0,
+__device__ __forceinline__ void orth_tile(const OrthProducts &p, const OrthPhase &f, int b0, int t, int &b, int &m0, int &n0,
                                           bool &below) {
   b = t / p.tiles[f.kind];
   t -= b * p.tiles[f.kind];
+  b += b0;
   if (f.kind != kOrthApply) {
     const int R = 256 / f.bn;
     int i = (int)((sqrtf(1.0f + 8.0f * (float)t / (float)R) - 1.0f) * 0.5f);
@@ -230,7 +235,40 @@ __device__ __forceinline__ void orth_load_half(uint32_t taddr, int n, uint32_t (
   for (int k = 0; k < 4; ++k) regs_fence(r[k >> 1][k & 1]);
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
+// Wait as mbar_wait_bounded for arrivals of the cluster's other CTAs, whose writes are then visible.
+__device__ __forceinline__ bool mbar_wait_cluster_bounded(uint64_t *bar, uint32_t parity, uint64_t budget,
+                                                          volatile int *abort_flag) {
+  const long long t0 = clock64();
+  while (true) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (*abort_flag) return false;
+    if ((uint64_t)(clock64() - t0) > budget) {
+      *abort_flag = 1;
+      record_device_error(kDevErrTimeout);
+      return false;
+    }
+  }
+}
+
+// Arrive, with this thread's writes, on the barrier at this offset in CTA `cta` of the cluster.
+__device__ __forceinline__ void mbar_arrive_cluster(uint64_t *bar, uint32_t cta) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(bar)), "r"(cta));
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+}
+
+// Launched in clusters of 2 (a cooperative grid, all matrices in every phase), or with CLUSTER of
+// p.cluster CTAs (cluster i has matrix i; no tile is split).
+template <bool CLUSTER>
+__global__ void __launch_bounds__(kOgThreads, 1)
     orth_products_kernel(const __grid_constant__ OrthMaps maps, const __grid_constant__ OrthProducts p) {
   constexpr int kStages = kOgStages;
   extern __shared__ uint8_t smem_raw[];
@@ -244,14 +282,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
   uint64_t *drain = acc_empty + 2;
   uint64_t *ready = drain + 1;                 // producer -> epilogue: the phase's inputs are written
   uint64_t *g_bars = ready + 1;                // [epilogue warps] G's entries of a Poly tile
-  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(g_bars + kOgEpiWarps);
+  uint64_t *phase_done = g_bars + kOgEpiWarps; // CLUSTER: the cluster's epilogue warps have finished the phase
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(phase_done + 1);
   volatile int *s_abort = reinterpret_cast<volatile int *>(s_tmem + 1);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t cta = cluster_ctarank();
+  const uint32_t rank = cta & 1;               // in the pair
   const bool is_leader = rank == 0;
-  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const uint16_t pair_mask = (uint16_t)(3u << (cta - rank));
+  const int pair = (int)(CLUSTER ? cta : blockIdx.x) >> 1;
+  const int npairs = (int)(CLUSTER ? (unsigned)p.cluster : gridDim.x) >> 1;
+  const int b0 = CLUSTER ? (int)blockIdx.x / p.cluster : 0;   // the first matrix
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
     for (int b = 0; b < 2; ++b) {
@@ -260,6 +303,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
     }
     mbar_init(drain, 1);
     mbar_init(ready, 1);
+    mbar_init(phase_done, (uint32_t)((CLUSTER ? p.cluster : 1) * kOgEpiWarps));
     for (int w = 0; w < kOgEpiWarps; ++w) mbar_init(&g_bars[w], 1);
     *s_abort = 0;
     fence_mbarrier_init();
@@ -273,9 +317,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // both CTAs' barriers exist before any cross-CTA arrive or byte count
+  cluster_sync();  // the cluster's barriers exist before any cross-CTA arrive or byte count
   tc_fence_after();
   const uint32_t tmem_base = *s_tmem;
+  if (CLUSTER) {
+    pdl_launch_dependents();
+    pdl_wait();
+  }
 
   if (warp == 0) {
     // ------------------------------------------------------ producer (both CTAs)
@@ -296,9 +344,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
       PairSchedule sched(f.split, pair, npairs, f.tiles, f.num_kt);
       int tile, kb, ke, b = 0, m0 = 0, n0 = 0;
       bool below, more = sched.next(tile, kb, ke);
-      if (more) orth_tile(p, f, tile, b, m0, n0, below);
-      bool up = true;
-      if (ph > 0 && lane < kOgEpiWarps)   // all of the phase before is written
+      if (more) orth_tile(p, f, b0, tile, b, m0, n0, below);
+      bool up = true;   // all of the phase before is written
+      if (CLUSTER) {
+        if (ph > 0) up = mbar_wait_cluster_bounded(phase_done, (uint32_t)(ph - 1) & 1u, p.wait_budget, s_abort);
+      } else if (ph > 0 && lane < kOgEpiWarps)
         up = flag_spin_bounded(p.counters + lane * kOgPhases + ph - 1, gridDim.x, p.wait_budget, s_abort);
       if (!__all_sync(0xFFFFFFFFu, up)) break;
       __syncwarp();
@@ -325,7 +375,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
             }
           }
           more = sched.next(tile, kb, ke);
-          if (more) orth_tile(p, f, tile, b, m0, n0, below);
+          if (more) orth_tile(p, f, b0, tile, b, m0, n0, below);
         }
       }
       ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
@@ -366,13 +416,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
           for (int kk = 0; kk < 4; ++kk)
             tc_mma_f16_pair(acc, a_desc0 + so + 2 * kk, b_desc0 + so + kk * b_step, idesc,
                             (kt != kb || kk != 0) ? 1u : 0u);
-          tc_commit_pair(&empty[s], 0x3);
+          tc_commit_pair(&empty[s], pair_mask);
         }
-        if (ok) tc_commit_pair(&acc_full[buf], 0x3);
+        if (ok) tc_commit_pair(&acc_full[buf], pair_mask);
       }
     }
     if (!ok) {
-      tc_commit_pair(drain, 0x1);
+      tc_commit_pair(drain, (uint16_t)(1u << cta));
       volatile int no_abort = 0;
       mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
     }
@@ -407,11 +457,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
       for (; alive && sched.next(tile, kb, ke); ++j) {
         int b, m0, n0;
         bool below;
-        orth_tile(p, f, tile, b, m0, n0, below);
+        orth_tile(p, f, b0, tile, b, m0, n0, below);
         m0 += (int)rank * 128 + 32 * q;
         n0 += f.bn / 2 * grp;
         const int halves = f.bn / 128;                        // pairs of chunks of this warp
-        const bool split = ke - kb < f.num_kt;
+        const bool split = !CLUSTER && ke - kb < f.num_kt;
         const int part = split ? pair % f.split : 0, parts = split ? f.split : 1;
         const int nch = min(2 * halves, (N - n0 + 31) >> 5);  // chunks inside the matrix (none: <= 0)
         const int buf = j & 1;
@@ -594,9 +644,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOgThreads, 1)
         }
       }
       __syncwarp();
-      if (alive && lane == 0) {   // this warp's stores of the phase are complete
-        bulk_wait_group<0>();
-        flag_add_release(p.counters + ew * kOgPhases + ph, 1u);
+      if (alive) {   // this warp's stores of the phase are complete
+        if (lane == 0) bulk_wait_group<0>();
+        if (CLUSTER) {
+          // A warp without a tile comes here early: its arrival counts for this phase only once the
+          // one before is over, which the producer knows first (and must have seen before this
+          // phase can end: the barrier tells two phases apart, not three).
+          const bool up = mbar_wait_bounded(ready, (uint32_t)ph & 1u, p.wait_budget, s_abort);
+          if (!__all_sync(0xFFFFFFFFu, up)) {
+            alive = false;
+            break;
+          }
+          __syncwarp();
+          if (lane < p.cluster) mbar_arrive_cluster(phase_done, (uint32_t)lane);
+        } else if (lane == 0) {
+          flag_add_release(p.counters + ew * kOgPhases + ph, 1u);
+        }
       }
     }
     if (lane == 0) {

@@ -660,19 +660,19 @@ struct OrthShape {
   double us;
 };
 
-double orth_stage_us(int bn, bool apply, int64_t use, int64_t P) {
-  const double share = (double)use / (double)P;
+double orth_stage_us(int bn, bool apply, int64_t use) {
+  const double share = (double)use / 74.0;
   return bn == 128 ? 0.25 + 0.10 * share : 0.31 + (apply ? 0.14 : 0.07) * share;
 }
 
-OrthShape orth_shape(int64_t tiles, int64_t kt, int64_t P, int bn, bool apply) {
+OrthShape orth_shape(int64_t tiles, int64_t kt, int64_t P, int bn, bool apply, int most) {
   OrthShape o = {bn, 1, tiles < P ? tiles : P, 0.0};
-  o.us = orth_stage_us(bn, apply, P, P) * (double)(tiles / P * kt) + (bn == 256 ? 2.4 : 1.4);
+  o.us = orth_stage_us(bn, apply, P) * (double)(tiles / P * kt) + (bn == 256 ? 2.4 : 1.4);
   const int64_t tail = tiles % P;
   if (tail) {
-    double least = orth_stage_us(bn, apply, tail, P) * (double)kt;
-    for (int64_t s = 2; s <= kOgMaxSplit && s <= kt && tail * s <= P; ++s) {
-      const double t = orth_stage_us(bn, apply, tail * s, P) * (double)((kt + s - 1) / s) + (bn == 256 ? 3.5 : 2.8) +
+    double least = orth_stage_us(bn, apply, tail) * (double)kt;
+    for (int64_t s = 2; s <= most && s <= kt && tail * s <= P; ++s) {
+      const double t = orth_stage_us(bn, apply, tail * s) * (double)((kt + s - 1) / s) + (bn == 256 ? 3.5 : 2.8) +
                        0.4 * (double)(s - 2);
       if (t < least) {
         least = t;
@@ -685,42 +685,110 @@ OrthShape orth_shape(int64_t tiles, int64_t kt, int64_t P, int bn, bool apply) {
   return o;
 }
 
-sp24_status launch_orth_products(const OrthMaps &maps, OrthProducts p, cudaStream_t stream) {
-  int64_t P = pairs_of<orth_products_kernel, kOgThreads, kOgSmem>();
-  if (P <= 0) return P == 0 ? SP24_ERR_CUDA : SP24_ERR_NO_DEVICE;
-  if (P > kOgMaxPairs) P = kOgMaxPairs;
-  const int64_t mb = (p.m + 255) / 256;
-  int64_t grid = 0;   // pairs: as many as the phase that uses most
+// Shapes of the three phases on P pairs for `batch` matrices; their time in sum, with what a
+// phase costs besides (waiting, first loads, counting: 4.5 us, or 3 us in a cluster).
+double orth_plan_phases(OrthProducts *p, int batch, int64_t P, bool cluster, int64_t *grid) {
+  const int64_t mb = (p->m + 255) / 256;
+  double us = 0.0;
+  *grid = 0;   // pairs: as many as the phase that uses most
   for (int k = 0; k < 3; ++k) {
     const bool apply = k == kOrthApply;
-    const int64_t kt = ((k == kOrthGram ? p.n : p.m) + 63) / 64;
+    const int64_t kt = ((k == kOrthGram ? p->n : p->m) + 63) / 64;
     OrthShape best = {};
     for (int bn = 128; bn <= 256; bn += 128) {
-      const int64_t per = apply ? mb * (((int64_t)p.n + bn - 1) / bn) : orth_sym_tiles(p.m, bn);
-      const OrthShape o = orth_shape(p.batch * per, kt, P, bn, apply);
+      const int64_t per = apply ? mb * (((int64_t)p->n + bn - 1) / bn) : orth_sym_tiles(p->m, bn);
+      const OrthShape o = orth_shape(batch * per, kt, P, bn, apply, cluster ? 1 : kOgMaxSplit);
       if (best.bn == 0 || o.us <= best.us) {
         best = o;
-        p.tiles[k] = (int)per;
+        p->tiles[k] = (int)per;
       }
     }
-    p.bn[k] = best.bn;
-    if (best.use > grid) grid = best.use;
+    p->bn[k] = best.bn;
+    us += best.us + (cluster ? 3.0 : 4.5);
+    if (best.use > *grid) *grid = best.use;
   }
   for (int k = 0; k < 3; ++k) {   // the splits on that many pairs
-    const int64_t kt = ((k == kOrthGram ? p.n : p.m) + 63) / 64;
-    p.split[k] = orth_shape((int64_t)p.batch * p.tiles[k], kt, grid, p.bn[k], k == kOrthApply).split;
+    const int64_t kt = ((k == kOrthGram ? p->n : p->m) + 63) / 64;
+    p->split[k] = orth_shape((int64_t)batch * p->tiles[k], kt, *grid, p->bn[k], k == kOrthApply, cluster ? 1 : kOgMaxSplit).split;
   }
+  return us;
+}
+
+// Clusters of C CTAs of the products kernel that fit at once (and its shared-memory opt-in).
+template <int C>
+int orth_clusters() {
+  static PerDevice cache;
+  const int dev = current_device();
+  if (dev < 0) return -1;
+  constexpr auto kernel = orth_products_kernel<true>;
+  std::call_once(cache.once[dev], [&] {
+    int n = 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(C);
+    cfg.blockDim = dim3(kOgThreads);
+    cfg.dynamicSmemBytes = kOgSmem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = C;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOgSmem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    cache.value[dev] = n;
+  });
+  return cache.value[dev];
+}
+
+sp24_status launch_orth_products(const OrthMaps &maps, OrthProducts p, cudaStream_t stream) {
+  int64_t P = pairs_of<orth_products_kernel<false>, kOgThreads, kOgSmem>();
+  if (P <= 0) return P == 0 ? SP24_ERR_CUDA : SP24_ERR_NO_DEVICE;
+  if (P > kOgMaxPairs) P = kOgMaxPairs;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * (unsigned)grid);
   cfg.blockDim = dim3(kOgThreads);
   cfg.dynamicSmemBytes = kOgSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr;   // its CTAs wait for one another: all are resident, or none starts
-  attr.id = cudaLaunchAttributeCooperative;
-  attr.val.cooperative = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, orth_products_kernel, maps, p) != cudaSuccess) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  int64_t grid = 0;
+  double least = orth_plan_phases(&p, p.batch, P, false, &grid);
+  // A cluster per matrix, of as many pairs as its phases use, where that is expected to be faster.
+  for (int c = 2; c <= 8; c *= 2) {
+    const int fit = c == 2 ? orth_clusters<2>() : (c == 4 ? orth_clusters<4>() : orth_clusters<8>());
+    if (fit <= 0) continue;
+    OrthProducts q = p;
+    int64_t use = 0;
+    const double us = orth_plan_phases(&q, 1, c / 2, true, &use) * (double)((p.batch + fit - 1) / fit);
+    if (us < least) {
+      least = us;
+      p = q;
+      p.cluster = c;
+    }
+  }
+  cudaError_t err;
+  if (p.cluster) {
+    cfg.gridDim = dim3((unsigned)(p.cluster * p.batch));
+    attr[0].val.clusterDim.x = (unsigned)p.cluster;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    p.batch = 1;
+    err = cudaLaunchKernelEx(&cfg, orth_products_kernel<true>, maps, p);
+  } else {
+    cfg.gridDim = dim3(2 * (unsigned)grid);
+    attr[0].val.clusterDim.x = 2;
+    attr[1].id = cudaLaunchAttributeCooperative;   // its CTAs wait for one another: all are resident, or none starts
+    attr[1].val.cooperative = 1;
+    err = cudaLaunchKernelEx(&cfg, orth_products_kernel<false>, maps, p);
+  }
+  if (err != cudaSuccess) {
     cudaGetLastError();
     return SP24_ERR_CUDA;
   }
