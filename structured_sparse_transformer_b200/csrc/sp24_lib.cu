@@ -686,7 +686,7 @@ OrthShape orth_shape(int64_t tiles, int64_t kt, int64_t P, int bn, bool apply, i
 }
 
 // Shapes of the three phases on P pairs for `batch` matrices; their time in sum, with what a
-// phase costs besides (waiting, first loads, counting: 4.5 us, or 3 us in a cluster).
+// phase costs besides (waiting, first loads, counting: 4.5 us, or 3.4 us in a cluster).
 double orth_plan_phases(OrthProducts *p, int batch, int64_t P, bool cluster, int64_t *grid) {
   const int64_t mb = (p->m + 255) / 256;
   double us = 0.0;
@@ -704,7 +704,7 @@ double orth_plan_phases(OrthProducts *p, int batch, int64_t P, bool cluster, int
       }
     }
     p->bn[k] = best.bn;
-    us += best.us + (cluster ? 3.0 : 4.5);
+    us += best.us + (cluster ? 3.4 : 4.5);
     if (best.use > *grid) *grid = best.use;
   }
   for (int k = 0; k < 3; ++k) {   // the splits on that many pairs

@@ -169,3 +169,37 @@ def test_quantized_layer_stays_near_the_16_bit_one():
     bound = 0.5 * (sx * w.double().abs().sum(1) + sw * x.double().abs().sum(1, keepdim=True)) + 0.25 * K * sx * sw
     bound = bound + ref.abs() * 2.0**-10
     assert ((y.cpu().double() - ref).abs() <= bound).all()
+
+
+def test_an_expired_wait_is_reported_and_the_next_call_is_right():
+    for T in (40, 700):
+        xq, sx, wq, sw = [t.cuda() for t in _operands(T, 1600, 528, 2)]
+        want, y = (torch.empty(T, 528, dtype=torch.float16, device="cuda") for _ in range(2))
+        sp.sp24_gemm_i8(xq, sx, wq, sw, want)
+        try:
+            sp.sp24_set_wait_budget(0)
+            sp.sp24_gemm_i8(xq, sx, wq, sw, y)
+            torch.cuda.synchronize()
+        finally:
+            sp.sp24_set_wait_budget(1 << 32)
+        assert sp.sp24_device_status() == 6
+        sp.sp24_gemm_i8(xq, sx, wq, sw, y)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and sp.sp24_device_status() == 0
+
+
+def test_outputs_past_32_bit_offsets():
+    """T N beyond 2^31 elements (5.4 GB): the last tokens are as in a small call, what lies behind is untouched."""
+    T, K, N = 40961, 64, 65552
+    g = torch.Generator(device="cuda").manual_seed(5)
+    xq = torch.randint(-127, 128, (T, K), generator=g, device="cuda").to(torch.int8)
+    wq = torch.randint(-127, 128, (N, K), generator=g, device="cuda").to(torch.int8)
+    sx = torch.rand(T, generator=g, device="cuda") * 0.01
+    sw = torch.rand(N, generator=g, device="cuda") * 0.01
+    y = torch.full((T + 1, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    sp.sp24_gemm_i8(xq, sx, wq, sw, y)
+    for lo, hi in ((0, 3), (T // 2, T // 2 + 3), (T - 3, T)):
+        part = torch.empty(hi - lo, N, dtype=torch.bfloat16, device="cuda")
+        sp.sp24_gemm_i8(xq[lo:hi].contiguous(), sx[lo:hi].contiguous(), wq, sw, part)
+        assert torch.equal(y[lo:hi], part)
+    assert (y[T:] == 7.0).all() and sp.sp24_device_status() == 0

@@ -229,17 +229,58 @@ def test_graph_replays_equal_eager_steps_on_a_side_stream():
     assert torch.equal(m, em) and torch.equal(w, ew) and torch.equal(w16, e16)
 
 
-def test_an_expired_wait_is_reported_and_the_next_call_is_right():
-    g = _grad((300, 300), 2)
+def test_two_streams_at_once():
+    """Independent calls side by side, each with its workspace: large (one cooperative grid each) and small ones."""
+    shapes = [(640, 1920), (1100, 520), (256, 512), (2, 64, 96)]
+    gs = [_grad(s, k) for k, s in enumerate(shapes)]
+    want = [_orth(g) for g in gs]
+    streams = [torch.cuda.Stream() for _ in shapes]
+    outs = [torch.empty(g.shape, dtype=torch.float16, device="cuda") for g in gs]
+    spaces = [_workspace(g) for g in gs]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for g, o, w, st in zip(gs, outs, spaces, streams):
+            sp.sp24_orthogonalize(g, o, w, stream=st)
+    torch.cuda.synchronize()
+    assert sp.sp24_device_status() == 0
+    for a, b in zip(outs, want):
+        assert torch.equal(a, b)
+
+
+def test_two_graphs_with_their_own_workspaces():
+    g = _grad((130, 200), 3)
     want = _orth(g)
-    try:
-        sp.sp24_set_wait_budget(0)
-        sp.sp24_orthogonalize(g, torch.empty(300, 300, dtype=torch.float16, device="cuda"), _workspace(g), steps=1)
-        torch.cuda.synchronize()
-    finally:
-        sp.sp24_set_wait_budget(1 << 32)
-    assert sp.sp24_device_status() == 6
-    assert torch.equal(_orth(g), want)
+    graphs, outs, spaces = [], [], []
+    for _ in range(2):
+        out, ws = torch.empty(130, 200, dtype=torch.float16, device="cuda"), _workspace(g)
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            sp.sp24_orthogonalize(g, out, ws)
+        graphs.append(gr)
+        outs.append(out)
+        spaces.append(ws)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for gr, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                gr.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want) and sp.sp24_device_status() == 0
+
+
+def test_an_expired_wait_is_reported_and_the_next_call_is_right():
+    for shape in ((700, 900), (64, 96)):       # a grid, a cluster
+        g = _grad(shape, 2)
+        want = _orth(g)
+        try:
+            sp.sp24_set_wait_budget(0)
+            sp.sp24_orthogonalize(g, torch.empty(*shape, dtype=torch.float16, device="cuda"), _workspace(g), steps=2)
+            torch.cuda.synchronize()
+        finally:
+            sp.sp24_set_wait_budget(1 << 32)
+        assert sp.sp24_device_status() == 6
+        assert torch.equal(_orth(g), want)
 
 
 def test_from_the_gradient_to_the_8_bit_layer():

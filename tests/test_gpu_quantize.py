@@ -119,3 +119,15 @@ def test_zero_sizes_streams_and_repeats():
     side.synchronize()
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
     assert np.array_equal(outs[0][0].cpu().numpy(), _reference(x.cpu())[0])
+
+
+@pytest.mark.parametrize("rows,cols", [(70001, 32768), (524289, 4104)])
+def test_matrices_past_32_bit_offsets(rows, cols):
+    """More than 2^31 entries: the last rows are as in a small call."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    q, s = torch.empty(rows, cols, dtype=torch.int8, device="cuda"), torch.empty(rows, device="cuda")
+    sp.sp24_quantize_rows(x, q, s)
+    for lo in (0, rows // 2, rows - 4):
+        qr, sr = _reference(x[lo:lo + 4].cpu())
+        assert np.array_equal(q[lo:lo + 4].cpu().numpy(), qr) and np.array_equal(s[lo:lo + 4].cpu().numpy(), sr)
