@@ -243,15 +243,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
 }
 
 // ------------------------------------------------------------------ few tokens
-// Up to 128 tokens: bound by reading Wq (and, for small ones, by latency), so the work is
-// spread over the weight alone.  A cluster of S CTAs (S = 1, 2, 4 or 8) computes 128 features x
-// all tokens, each CTA an S-th of K: M = 128, N = TP MMAs (cta_group::1) on tiles that one
-// thread loads as fast as the ring of stages takes them.  The 32-bit integer partial sums
+// Where the 256-feature tiles above would leave most pairs idle (up to 128 tokens, or more with a
+// small weight): bound by reading Wq and by latency, so K is spread too.  A cluster of S CTAs
+// (S = 1, 2, 4 or 8) computes 128 features x TP tokens, each CTA an S-th of K: M = 128, N = TP
+// MMAs (cta_group::1) on tiles that one thread loads as fast as the ring of stages takes them.  The 32-bit integer partial sums
 // meet through distributed shared memory: each CTA leaves its own in shared memory, and CTA r
 // adds all of them for tokens r, r + S, ..., scales and stores (integer sums: the order does
 // not matter).
 // At T = 1, K = 1600, N = 6400 the two-CTA tile above took 7.1 us with 25 CTA pairs reading.
-constexpr int kI8sThreads = 192;                       // producer, MMA, four epilogue warps
+constexpr int kI8sThreads = 64 + 256;                  // producer, MMA, eight epilogue warps
 constexpr int kI8sMaxStages = 8;
 
 template <int TP>
@@ -291,12 +291,10 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
       : "memory");
 }
 
-// The word at this shared-memory address in CTA `cta` of the cluster.
-__device__ __forceinline__ int ld_cluster_s32(uint32_t saddr, uint32_t cta) {
-  uint32_t remote;
+// The word at this shared::cluster address (not ordered against other loads).
+__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
   int v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(saddr), "r"(cta));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
 
@@ -320,7 +318,10 @@ __global__ void __launch_bounds__(kI8sThreads)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rank = blockIdx.x % split;
-  const int f0 = (blockIdx.x / split) * 128;
+  const int f0 = (blockIdx.x / split) * 128, t0 = blockIdx.y * TP;
+  T = min(T - t0, TP);   // tokens of this tile
+  sx += t0;
+  Y += (int64_t)t0 * N;
   const int kb = (int)((int64_t)rank * num_kt / split), ke = (int)((int64_t)(rank + 1) * num_kt / split);
   constexpr uint32_t kCols = TP < 32 ? 32 : TP;
 
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(kI8sThreads)
       uint8_t *st = smem + s * G::kStageBytes;
       mbar_arrive_expect_tx(&full[s], G::kStageBytes);
       tma_load_2d(st, &tm_w, &full[s], kt * 128, f0);
-      tma_load_2d(st + G::kSmemW, &tm_x, &full[s], kt * 128, 0);
+      tma_load_2d(st + G::kSmemW, &tm_x, &full[s], kt * 128, t0);
     }
     for (int i = g > stages ? g - stages : 0; i < g; ++i) {   // every copy lands before the block ends
       volatile int no_abort = 0;
@@ -383,28 +384,49 @@ __global__ void __launch_bounds__(kI8sThreads)
       mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
     }
   } else if (warp >= 2) {
-    const int q = warp & 3, f = 32 * q + lane;   // this lane's feature of the tile
+    // This lane's feature of the tile; the two warps of a lane quadrant take tokens in turn.
+    const int q = warp & 3, f = 32 * q + lane, turn = (warp - 2) >> 2;
     const float w = f0 + f < N ? __ldg(sw + f0 + f) : 0.0f;
-    auto put = [&](int t, int acc) {
-      const float v = (__int2float_rn(acc) * w) * __ldg(sx + t);
-      const float2 y = GELU ? gelu2(make_float2(v, v)) : make_float2(v, v);
-      Y[(int64_t)t * N + f0 + f] = (uint16_t)f32_to_bits<BF16>(y.x);
+    // kB sums of one feature, tokens t, t + step, ...: all scales are loaded before any is used.
+    // (Two at a time where there are few tokens: a short kernel's time is also that of fetching its
+    // code.)
+    constexpr int kB = TP <= 32 ? 2 : 8;
+    auto put = [&](int t, int step, const int (&acc)[kB]) {
+      float x[kB];
+#pragma unroll
+      for (int i = 0; i < kB; ++i) x[i] = t + i * step < T ? __ldg(sx + t + i * step) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < kB; i += 2) {
+        float2 y = make_float2((__int2float_rn(acc[i]) * w) * x[i], (__int2float_rn(acc[i + 1]) * w) * x[i + 1]);
+        if (GELU) y = gelu2(y);
+        const uint32_t v = pack2<BF16>(y.x, y.y);
+        uint16_t *at = Y + (int64_t)(t + i * step) * N + f0 + f;
+        if (t + i * step < T) at[0] = (uint16_t)(v & 0xFFFFu);
+        if (t + (i + 1) * step < T) at[(int64_t)step * N] = (uint16_t)(v >> 16);
+      }
     };
     const bool got = mbar_wait_bounded(acc_full, 0, wait_budget, s_abort);
     done = __all_sync(0xFFFFFFFFu, got);
     if (done) {
       tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < T; c += 16) {
+      for (int c = 16 * turn; c < T; c += 32) {
         uint32_t r[16];
         tmem_ld_32x32b_x16(tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)c, r);
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));   // uses stay below the wait
+        if (split > 1) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          if (split > 1) part[(c + i) * 128 + f] = (int)r[i];
-          else if (c + i < T && f0 + f < N) put(c + i, (int)r[i]);
+          for (int i = 0; i < 16; ++i) part[(c + i) * 128 + f] = (int)r[i];
+        } else if (f0 + f < N) {
+#pragma unroll
+          for (int i = 0; i < 16; i += kB) {
+            int v[kB];
+#pragma unroll
+            for (int e = 0; e < kB; ++e) v[e] = (int)r[i + e];
+            if (c + i < T) put(c + i, 1, v);
+          }
         }
       }
     }
@@ -412,14 +434,27 @@ __global__ void __launch_bounds__(kI8sThreads)
     if (split > 1) {
       cluster_sync();   // every CTA's sums are in its shared memory
       if (done && f0 + f < N) {
+        // kB tokens at a time, four CTAs' words of them in flight together.
 #pragma unroll 1
-        for (int t = rank; t < T; t += split) {
-          const uint32_t at = smem_u32(part + t * 128 + f);
-          int sum = 0;
+        for (int t = rank + kB * split * turn; t < T; t += 2 * kB * split) {
+          int sum[kB] = {};
+#pragma unroll 1
+          for (int c0 = 0; c0 < split; c0 += 4) {
+            int v[4][kB];
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            if (c < split) sum += ld_cluster_s32(at, (uint32_t)c);
-          put(t, sum);
+            for (int c = 0; c < 4; ++c) {
+              uint32_t remote;
+              asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(part + f)), "r"(min(c0 + c, split - 1)));
+#pragma unroll
+              for (int i = 0; i < kB; ++i)
+                v[c][i] = c0 + c < split && t + i * split < T ? ld_cluster_s32(remote + 512u * (uint32_t)(t + i * split)) : 0;
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int i = 0; i < kB; ++i) sum[i] += v[c][i];
+          }
+          put(t, split, sum);
         }
       }
     }
