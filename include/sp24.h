@@ -17,6 +17,9 @@
  *   - abstract and Experiment Setup row: dense fine-tuning for the last 1/6 of
  *     the steps (sp24_gemm_dense, sp24_gemm_dgrad_dense, sp24_gemm_wgrad_dense,
  *     sp24_transpose).
+ * Beside the method: the optimiser's step on these gradients and weights
+ * (sp24_orthogonalize, sp24_muon_step) and the trained layer's 8-bit forward
+ * (sp24_quantize_rows, sp24_gemm_i8).
  *
  * Conventions shared by every call
  *   - Matrices are row-major.  W is [rows x cols] with leading dimension ldw
@@ -464,7 +467,8 @@ SP24_API sp24_status sp24_quantize_rows(const void *X, sp24_dtype dtype, int64_t
  * inference counterpart of sp24_gemm_fwd / sp24_gemm_dense:
  *   Y[t][n] = (sum_k Xq[t][k] Wq[n][k]) * sw[n] * sx[t],  optionally gelu of it
  * The sum is exact (32-bit integers); then two fp32 products in that order, the
- * GELU (exact erf form) in fp32, and one rounding to dtype.
+ * GELU (exact erf form) in fp32, and one rounding to dtype.  A token's result does
+ * not depend on the others in the call.
  *   Xq  device int8 [T x K], sx device fp32 [T] (sp24_quantize_rows of X)
  *   Wq  device int8 [N x K], sw device fp32 [N] (of W, or of W with its mask)
  *   Y   device dtype [T x N], overwritten

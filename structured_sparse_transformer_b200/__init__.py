@@ -12,7 +12,10 @@ Operations from "Accelerating Transformer Pre-training with 2:4 Sparsity":
 transposable 2:4 mask search (reproducibility table, Pseudocode row,
 Algorithm 1), pruning/compression and the 2:4 sparse FFN GEMMs (Software
 Dependencies row), masked decay and flip rate (abstract), and the dense GEMM
-of the dense fine-tuning phase (abstract; Experiment Setup row).
+of the dense fine-tuning phase (abstract; Experiment Setup row).  Beside them, what a
+training program needs next to those gradients and weights: the Muon optimiser's step
+(momentum, Newton-Schulz orthogonalisation, update) and the 8-bit forward product with
+its row-wise quantisation.
 """
 from __future__ import annotations
 

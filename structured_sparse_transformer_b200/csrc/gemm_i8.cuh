@@ -15,6 +15,7 @@
 // is bounded.
 #pragma once
 #include "gemm_sp.cuh"
+#include "sp24_ops.cuh"
 
 namespace sp24 {
 
@@ -269,35 +270,6 @@ struct I8sGeom {
   static_assert(smem_for(kStagesMost) <= 232448 && 8 * (2 * kI8sMaxStages + 2) + 16 <= kBarBytes, "shared memory per CTA");
 };
 
-// Dense 8-bit integer MMA of one CTA (M = 128).
-__device__ __forceinline__ void tc_mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// 32 lanes x 16 columns: lane i of the warp receives its tensor-memory lane's columns.
-__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-      "[%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-
-// The word at this shared::cluster address (not ordered against other loads).
-__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
-
 template <int TP, bool BF16, bool GELU>
 __global__ void __launch_bounds__(kI8sThreads)
     gemm_i8_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, int N, int T,
@@ -414,8 +386,7 @@ __global__ void __launch_bounds__(kI8sThreads)
         uint32_t r[16];
         tmem_ld_32x32b_x16(tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)c, r);
         tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));   // uses stay below the wait
+        regs_fence(r);
         if (split > 1) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) part[(c + i) * 128 + f] = (int)r[i];
@@ -443,8 +414,7 @@ __global__ void __launch_bounds__(kI8sThreads)
             int v[4][kB];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              uint32_t remote;
-              asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(part + f)), "r"(min(c0 + c, split - 1)));
+              const uint32_t remote = cluster_addr(smem_u32(part + f), (uint32_t)min(c0 + c, split - 1));
 #pragma unroll
               for (int i = 0; i < kB; ++i)
                 v[c][i] = c0 + c < split && t + i * split < T ? ld_cluster_s32(remote + 512u * (uint32_t)(t + i * split)) : 0;
@@ -475,7 +445,7 @@ __global__ void __launch_bounds__(kI8sThreads)
   }
 }
 
-// ------------------------------------------------------------------ one to four tokens
+// ------------------------------------------------------------------ one to eight tokens
 // Bound by reading Wq once, and by latency: no tensor memory, no barriers, no tensor maps to
 // encode on the host.  A block takes four features; a thread takes every 128th 16-byte unit of
 // K for all four and TT tokens (dp4a, exact), so each unit of Xq serves four rows of Wq.

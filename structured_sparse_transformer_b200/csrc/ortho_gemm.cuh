@@ -43,6 +43,7 @@
 // latency is paid four times (3.6 us a tile).  Every wait is bounded.
 #pragma once
 #include "gemm_sp.cuh"
+#include "sp24_ops.cuh"
 
 namespace sp24 {
 
@@ -136,70 +137,6 @@ __device__ __forceinline__ void orth_tile(const OrthProducts &p, const OrthPhase
   }
 }
 
-// Four 8x8 16-bit matrices, as held (no transpose): register j of thread t is row t/4,
-// columns 2(t%4) and 2(t%4)+1 of matrix j; lane 8j + r gives the address of its row r.
-__device__ __forceinline__ void stmatrix_x4(uint32_t saddr, const uint32_t (&r)[4]) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3])
-               : "memory");
-}
-
-// The reverse of stmatrix_x4.
-__device__ __forceinline__ void ldmatrix_x4(uint32_t saddr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(saddr)
-               : "memory");
-}
-
-// 16 tensor-memory lanes x 32 columns: tmem_ld_16x256b_x2's layout over four 8-column blocks.
-__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-      "[%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-
-// TMA tile load into this CTA's shared memory, counted on its own mbarrier.
-__device__ __forceinline__ void tma_load_3d(void *smem_dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
-
-// Wait until *flag >= target without sleeping (the phase's start waits on it).
-__device__ __forceinline__ bool flag_spin_bounded(const unsigned *flag, unsigned target, uint64_t budget,
-                                                  volatile int *abort_flag) {
-  if (flag_load_acquire(flag) >= target) return true;
-  const long long t0 = clock64();
-  while (true) {
-    if (*abort_flag) return false;
-    if ((uint64_t)(clock64() - t0) > budget) {
-      *abort_flag = 1;
-      record_device_error(kDevErrTimeout);
-      return false;
-    }
-    if (flag_load_acquire(flag) >= target) return true;
-  }
-}
-
-__device__ __forceinline__ void flag_store_release(unsigned *flag, unsigned v) {
-  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(flag), "r"(v) : "memory");
-}
-
-__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
-
-// Uses of the loaded registers stay below the wait.
-__device__ __forceinline__ void regs_fence(uint32_t (&r)[16]) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));
-}
-
 // Passes on a warp's chunks that other parts finish.  Not inlined: inlined, the compiler keeps
 // its registers beside the epilogue's and spills.
 __device__ __noinline__ void orth_pass_chunks(uint32_t taddr, int nch, int halves, int part, int parts, float4 *slot) {
@@ -233,36 +170,6 @@ __device__ __forceinline__ void orth_load_half(uint32_t taddr, int n, uint32_t (
   tmem_wait_ld();
 #pragma unroll
   for (int k = 0; k < 4; ++k) regs_fence(r[k >> 1][k & 1]);
-}
-
-// Wait as mbar_wait_bounded for arrivals of the cluster's other CTAs, whose writes are then visible.
-__device__ __forceinline__ bool mbar_wait_cluster_bounded(uint64_t *bar, uint32_t parity, uint64_t budget,
-                                                          volatile int *abort_flag) {
-  const long long t0 = clock64();
-  while (true) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (done) return true;
-    if (*abort_flag) return false;
-    if ((uint64_t)(clock64() - t0) > budget) {
-      *abort_flag = 1;
-      record_device_error(kDevErrTimeout);
-      return false;
-    }
-  }
-}
-
-// Arrive, with this thread's writes, on the barrier at this offset in CTA `cta` of the cluster.
-__device__ __forceinline__ void mbar_arrive_cluster(uint64_t *bar, uint32_t cta) {
-  uint32_t remote;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(bar)), "r"(cta));
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
 }
 
 // Launched in clusters of 2 (a cooperative grid, all matrices in every phase), or with CLUSTER of

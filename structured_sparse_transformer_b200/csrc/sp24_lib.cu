@@ -978,12 +978,13 @@ sp24_status launch_i8_few(const int8_t *Xq, int64_t T, int64_t K, const int8_t *
 template <bool BF16, bool GELU>
 sp24_status launch_i8(const int8_t *Xq, int64_t T, int64_t K, const int8_t *Wq, int64_t N, void *Y, const float *sx,
                       const float *sw, cudaStream_t s) {
-  if (T <= 4) {
+  if (T <= 8) {
     const dim3 grid((unsigned)(N / kI8vRows));
     uint16_t *y = static_cast<uint16_t *>(Y);
     return T == 1   ? launch_pdl(gemv_i8_kernel<1, BF16, GELU>, grid, dim3(kI8vThreads), 0, s, Xq, sx, (int)T, (int)K, Wq, sw, (int)N, y)
            : T == 2 ? launch_pdl(gemv_i8_kernel<2, BF16, GELU>, grid, dim3(kI8vThreads), 0, s, Xq, sx, (int)T, (int)K, Wq, sw, (int)N, y)
-                    : launch_pdl(gemv_i8_kernel<4, BF16, GELU>, grid, dim3(kI8vThreads), 0, s, Xq, sx, (int)T, (int)K, Wq, sw, (int)N, y);
+           : T <= 4 ? launch_pdl(gemv_i8_kernel<4, BF16, GELU>, grid, dim3(kI8vThreads), 0, s, Xq, sx, (int)T, (int)K, Wq, sw, (int)N, y)
+                    : launch_pdl(gemv_i8_kernel<8, BF16, GELU>, grid, dim3(kI8vThreads), 0, s, Xq, sx, (int)T, (int)K, Wq, sw, (int)N, y);
   }
   if (T <= 16) return launch_i8_few<16, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);
   if (T <= 32) return launch_i8_few<32, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);

@@ -11,7 +11,10 @@ T = --tokens rows of N(0, 1) activations: gemm_fwd computes [T x rows] from
 [rows x cols] weight gradient from dY [T x rows] (MVUE-sparsified) and
 X [T x cols] (gemm_wgrad_decay: with the masked decay of W's mask in its epilogue;
 gemm_wgrad_dense: dY dense, read as stored); mvue sparsifies dY [T x rows] (bytes per dY
-element).  Each timed launch follows an
+element).  muon_step is one optimiser step on fp32 [rows x cols] and orthogonalize its
+Newton-Schulz part alone (flops of five rounds, a symmetric product counted at half);
+quantize takes [rows x cols] to 8 bits, gemm_i8 is the 8-bit forward product [T x rows] from
+[T x cols] (--epi gelu: behind a GELU).  Each timed launch follows an
 L2 flush (256 MiB write) and is timed alone with CUDA events on the current
 stream.  Prints one JSON line: average microseconds per launch and the
 algorithmic throughput (bytes for the memory-bound kernels, dense-equivalent
@@ -35,6 +38,7 @@ BYTES_PER_ELEMENT = {
     "flip": 2 / 16,                                  # read two indices
     "transpose": 4,                                  # read W, write W^T
     "mvue": 2 + 1 + 1 / 8,                           # read dY; write kept values and metadata
+    "quantize": 2 + 1,                               # read X, write the 8-bit values
 }
 
 
@@ -42,7 +46,8 @@ def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--kernel", required=True,
                     choices=sorted(BYTES_PER_ELEMENT) + ["gemm_fwd", "gemm_dgrad", "gemm_dense_fwd", "gemm_dense_dgrad",
-                                                         "gemm_wgrad", "gemm_wgrad_decay", "gemm_wgrad_dense"])
+                                                         "gemm_wgrad", "gemm_wgrad_decay", "gemm_wgrad_dense",
+                                                         "gemm_i8", "muon_step", "orthogonalize"])
     ap.add_argument("--rows", type=int, required=True)
     ap.add_argument("--cols", type=int, required=True)
     ap.add_argument("--tokens", type=int, default=8192)
@@ -114,6 +119,25 @@ def main(argv=None):
         x = torch.randn(T, C, device=dev, generator=gen).to(tdt)
         dw = torch.empty(R, C, dtype=torch.float32, device=dev)
         fn = lambda: sp.sp24_gemm_wgrad_dense(x, dy, dw)
+    elif k in ("muon_step", "orthogonalize"):
+        g = torch.randn(R, C, device=dev, generator=gen) * 1e-3
+        ws = torch.empty(sp.sp24_orthogonalize_size(R, C), dtype=torch.uint8, device=dev)
+        if k == "orthogonalize":
+            fn = lambda: sp.sp24_orthogonalize(g, w, ws)
+        else:
+            m, w32 = torch.zeros_like(g), w.float()
+            fn = lambda: sp.sp24_muon_step(g, m, w32, w, ws, lr=1e-3, weight_decay=0.1)
+    elif k == "quantize":
+        q, sc = torch.empty(R, C, dtype=torch.int8, device=dev), torch.empty(R, device=dev)
+        fn = lambda: sp.sp24_quantize_rows(w, q, sc)
+    elif k == "gemm_i8":
+        x = torch.randn(T, C, device=dev, generator=gen).to(tdt)
+        xq, sx = torch.empty(T, C, dtype=torch.int8, device=dev), torch.empty(T, device=dev)
+        wq, sw = torch.empty(R, C, dtype=torch.int8, device=dev), torch.empty(R, device=dev)
+        sp.sp24_quantize_rows(x, xq, sx)
+        sp.sp24_quantize_rows(w, wq, sw, prev)
+        y = torch.empty(T, R, dtype=tdt, device=dev)
+        fn = lambda: sp.sp24_gemm_i8(xq, sx, wq, sw, y, "gelu" if args.epi == "gelu" else None)
     elif k == "transpose":
         wt = torch.empty(C, R, dtype=tdt, device=dev)
         fn = lambda: sp.sp24_transpose(w, wt)
@@ -160,6 +184,9 @@ def main(argv=None):
     avg_s = total / args.iters * 1e-3
     if k.startswith("gemm"):
         amount, unit = 2.0 * T * R * C / avg_s / 1e12, "TFLOP/s"
+    elif k in ("muon_step", "orthogonalize"):
+        lo, hi = min(R, C), max(R, C)
+        amount, unit = 5.0 * (lo * (lo + 1.0) * hi + lo * lo * (lo + 1.0) + 2.0 * lo * lo * hi) / avg_s / 1e12, "TFLOP/s"
     elif k == "mvue":
         amount, unit = T * R * BYTES_PER_ELEMENT[k] / avg_s / 1e9, "GB/s"
     else:
