@@ -9,9 +9,9 @@
 //
 // orth_products_kernel is one cooperative launch of CTA pairs (tcgen05 cta_group::2, 256 x 256
 // tiles, fp16 operands, fp32 accumulation) that runs all other phases one after another.  A
-// phase needs everything the one before wrote, so at its end every epilogue warp counts up a
-// counter of the phase once its stores are complete, and every TMA producer waits for the
-// counts: only the producers stall, tensor memory, barriers and descriptors stay set up.
+// phase needs everything the one before wrote, so at its end every CTA counts up a counter of
+// the phase once its epilogue warps' stores are complete, and every TMA producer waits for the
+// count: only the producers stall, tensor memory, barriers and descriptors stay set up.
 // (As 15 launches, each phase paid for launch, set-up and drain: about 9 us each.)
 // Small matrices (CLUSTER) take a cluster of CTA pairs each instead: they need not wait for one
 // another, no cooperative launch is needed, and the counts become arrivals on an mbarrier of
@@ -64,14 +64,11 @@ constexpr int kOgMaxSteps = 16;
 // Partial sums of one CTA of a split tile: per epilogue warp and chunk, the registers of its
 // tensor-memory load as eight float4 per lane.
 constexpr int64_t kOgPartFloats = (int64_t)kOgEpiWarps * kOgChunks * 8 * 32 * 4;
-// Counters at the front of the workspace, zero at launch: per epilogue warp and phase, the CTAs
-// whose warp has finished it (one counter per warp, so that each warp releases its own stores
-// and no address takes more than one increment per CTA); then per (CTA, epilogue warp), 1 +
-// the last phase whose partial sums it has passed on.
-constexpr int kOgPhases = 64;
-constexpr int kOgPhaseCounters = kOgPhases * kOgEpiWarps;
+// Counters at the front of the workspace, zero at launch: per phase, the CTAs that have finished
+// it; then per (CTA, epilogue warp), 1 + the last phase whose partial sums it has passed on.
+constexpr int kOgPhaseCounters = 64;
 constexpr int kOgCounters = kOgPhaseCounters + 2 * kOgMaxPairs * kOgEpiWarps;
-static_assert(3 * kOgMaxSteps <= kOgPhases, "a counter per phase");
+static_assert(3 * kOgMaxSteps <= kOgPhaseCounters, "a counter per phase");
 static_assert(kOgSmem <= 232448 && 8 * (2 * kOgStages + 7 + kOgEpiWarps) <= kOgBarBytes,
               "shared memory per CTA");
 
@@ -234,8 +231,7 @@ __global__ void __launch_bounds__(kOgThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------ producer (both CTAs)
-    // Lane w waits for the epilogue warps w of every CTA; lane 0 issues the loads.  What does not
-    // depend on the phase before is done ahead of the wait.
+    // What does not depend on the phase before is done ahead of the wait for it.
     uint32_t g = 0;
     bool ok = true;
     for (int ph = 0; ok && ph < p.phases; ++ph) {
@@ -255,8 +251,9 @@ __global__ void __launch_bounds__(kOgThreads, 1)
       bool up = true;   // all of the phase before is written
       if (CLUSTER) {
         if (ph > 0) up = mbar_wait_cluster_bounded(phase_done, (uint32_t)(ph - 1) & 1u, p.wait_budget, s_abort);
-      } else if (ph > 0 && lane < kOgEpiWarps)
-        up = flag_spin_bounded(p.counters + lane * kOgPhases + ph - 1, gridDim.x, p.wait_budget, s_abort);
+      } else if (ph > 0 && lane == 0) {
+        up = flag_spin_bounded(p.counters + ph - 1, gridDim.x, p.wait_budget, s_abort);
+      }
       if (!__all_sync(0xFFFFFFFFu, up)) break;
       __syncwarp();
       if (lane == 0) {
@@ -354,7 +351,7 @@ __global__ void __launch_bounds__(kOgThreads, 1)
     unsigned *flag_own = p.counters + kOgPhaseCounters + (int64_t)blockIdx.x * kOgEpiWarps + ew;
     bool alive = true;
     int j = 0;
-    for (int ph = 0; alive && ph < p.phases; ++ph) {
+    for (int ph = 0; ph < p.phases; ++ph) {   // (to the end, with or without work: its barrier counts all warps)
       const OrthPhase f(p, ph);
       const CUtensorMap *mo = f.kind == kOrthGram ? &maps.g_st : (f.kind == kOrthPoly ? &maps.p_st : &maps.x_st[1 - f.in]);
       const int N = f.kind == kOrthApply ? p.n : p.m;
@@ -551,22 +548,18 @@ __global__ void __launch_bounds__(kOgThreads, 1)
         }
       }
       __syncwarp();
-      if (alive) {   // this warp's stores of the phase are complete
-        if (lane == 0) bulk_wait_group<0>();
-        if (CLUSTER) {
-          // A warp without a tile comes here early: its arrival counts for this phase only once the
-          // one before is over, which the producer knows first (and must have seen before this
-          // phase can end: the barrier tells two phases apart, not three).
-          const bool up = mbar_wait_bounded(ready, (uint32_t)ph & 1u, p.wait_budget, s_abort);
-          if (!__all_sync(0xFFFFFFFFu, up)) {
-            alive = false;
-            break;
-          }
-          __syncwarp();
-          if (lane < p.cluster) mbar_arrive_cluster(phase_done, (uint32_t)lane);
-        } else if (lane == 0) {
-          flag_add_release(p.counters + ew * kOgPhases + ph, 1u);
-        }
+      if (lane == 0) bulk_wait_group<0>();   // this warp's stores of the phase are complete
+      if (!CLUSTER) {
+        named_barrier_sync(1, 32 * kOgEpiWarps);
+        if (ew == 0 && lane == 0 && alive) flag_add_release(p.counters + ph, 1u);
+      } else if (alive) {
+        // A warp without a tile comes here early: its arrival counts for this phase only once the
+        // one before is over, which the producer knows first (and must have seen before this
+        // phase can end: the barrier tells two phases apart, not three).
+        const bool up = mbar_wait_bounded(ready, (uint32_t)ph & 1u, p.wait_budget, s_abort);
+        alive = __all_sync(0xFFFFFFFFu, up);
+        __syncwarp();
+        if (alive && lane < p.cluster) mbar_arrive_cluster(phase_done, (uint32_t)lane);
       }
     }
     if (lane == 0) {
@@ -603,7 +596,7 @@ struct OrthLast {
 constexpr int kOlEpiWarps = 16;
 constexpr int kOlThreads = 64 + 32 * kOlEpiWarps;
 constexpr int kOlStages = 6;
-constexpr int kOlSmem = kOlStages * kOgStageBytes + kOgBarBytes + 1024;
+constexpr int kOlSmem = kOlStages * kOgStageBytes + kOgBarBytes + 1024;   // (stages sized for BN = 256)
 
 // 32 rows of a column with pitch ld, `left` of them inside the matrix (the last one repeats).
 __device__ __forceinline__ void orth_load_rows(const float *src, int ld, int left, float (&v)[32]) {
@@ -611,12 +604,12 @@ __device__ __forceinline__ void orth_load_rows(const float *src, int ld, int lef
   for (int i = 0; i < 32; ++i, src += i < left ? ld : 0) v[i] = __ldcs(src);
 }
 
-// Lane = column of the matrix, accumulator column = row.  Persistent over 256 x 256 tiles, two
-// accumulators.  16 epilogue warps take 32 columns x 64 rows of the tile each, in two chunks of
-// 32 rows; the first chunk's W is loaded before the accumulator is ready, the second's before
-// the first is stored, so 64 KB of W per SM are in flight behind the main loop.  Bound, with
-// UPDATE, by memory: 10 bytes per entry.
-template <bool BF16, bool UPDATE, bool TALL>
+// Lane = column of the matrix, accumulator column = row.  Persistent over tiles of 256 columns x
+// BN rows, two accumulators; BN = 128 where there would be few tiles.  16 epilogue warps take 32
+// columns x BN/4 rows of the tile each, in chunks of 32 rows; the first chunk's W is loaded before
+// the accumulator is ready, the second's before the first is stored, so 64 KB of W per SM are in
+// flight behind the main loop.  Bound, with UPDATE, by memory: 10 bytes per entry.
+template <bool BF16, bool UPDATE, bool TALL, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOlThreads, 1)
     orth_last_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                      const OrthLast p) {
@@ -668,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOlThreads, 1)
     b = tile / p.tiles;
     const int t = tile - b * p.tiles;
     m0 = (t % num_mt) * 256;
-    n0 = (t / num_mt) * 256;
+    n0 = (t / num_mt) * BN;
   };
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------ producer (both CTAs)
@@ -677,7 +670,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOlThreads, 1)
     for (int tile = pair; ok && tile < num_tiles; tile += npairs) {
       int b, m0, n0;
       tile_at(tile, b, m0, n0);
-      const int a_row = m0 + (int)rank * 128, b_row = n0 + (int)rank * 128;
+      const int a_row = m0 + (int)rank * 128, b_row = n0 + (int)rank * (BN / 2);
       for (int kt = 0; kt < p.num_kt; ++kt, ++g) {
         const int s = (int)(g % kStages);
         if (!mbar_wait_bounded(&empty[s], ((g / kStages) & 1u) ^ 1u, p.wait_budget, s_abort)) {
@@ -685,12 +678,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOlThreads, 1)
           break;
         }
         uint8_t *st = smem + s * kOgStageBytes;
-        if (is_leader) mbar_arrive_expect_tx(&full[s], 2 * kOgStageBytes);
+        if (is_leader) mbar_arrive_expect_tx(&full[s], 2 * (16384 + 64 * BN));
         // P K-major, X in two 64-column atoms of 64 rows.
         if (TALL) {
           tma_load_3d_pair(st, &tm_a, &full[s], kt * 64, a_row, b);
           tma_load_3d_pair(st + 16384, &tm_b, &full[s], b_row, kt * 64, b);
-          tma_load_3d_pair(st + 24576, &tm_b, &full[s], b_row + 64, kt * 64, b);
+          if (BN == 256) tma_load_3d_pair(st + 24576, &tm_b, &full[s], b_row + 64, kt * 64, b);
         } else {
           tma_load_3d_pair(st, &tm_a, &full[s], a_row, kt * 64, b);
           tma_load_3d_pair(st + 8192, &tm_a, &full[s], a_row + 64, kt * 64, b);
@@ -707,7 +700,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOlThreads, 1)
     }
   } else if (warp == 1 && lane == 0 && is_leader) {
     // ----------------------------------------------------- MMA issuer (leader)
-    constexpr uint32_t idesc = make_idesc_dense(false, 256, 256) | (TALL ? 1u << 16 : 1u << 15);
+    constexpr uint32_t idesc = make_idesc_dense(false, 256, BN) | (TALL ? 1u << 16 : 1u << 15);
     const uint64_t a_desc0 = smem_desc(smem_u32(smem), TALL ? 16 : 8192, 1024, kSwizzle128B);
     const uint64_t b_desc0 = smem_desc(smem_u32(smem + 16384), TALL ? 8192 : 16, 1024, kSwizzle128B);
     uint32_t g = 0;
@@ -746,7 +739,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOlThreads, 1)
       int b, m0, n0;
       tile_at(tile, b, m0, n0);
       const int col = m0 + (int)rank * 128 + 32 * q + lane;
-      const int row0 = n0 + 64 * grp;
+      const int row0 = n0 + BN / 4 * grp;
       const int left = p.rows - row0;   // rows of the matrix from this warp's first on
       const int64_t at = ((int64_t)b * p.rows + row0) * p.cols;
       const float alpha = p.gamma ? p.alpha * __ldg(p.gamma + b) : p.alpha;
@@ -760,15 +753,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOlThreads, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t t_base = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * 256 + 64 * grp);
+      const uint32_t t_base = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * 256 + BN / 4 * grp);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < BN / 128; ++k) {
         uint32_t r[32];
         tmem_ld_32x32b_x32(t_base + (uint32_t)(32 * k), r);
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));   // uses stay below the wait
-        if (k == 1) {   // the accumulator goes back to the MMA
+        if (k == BN / 128 - 1) {   // the accumulator goes back to the MMA
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_leader(&acc_empty[buf]);
@@ -778,7 +771,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOlThreads, 1)
           const float acc = __uint_as_float(r[i]);
           r[i] = __float_as_uint(UPDATE ? fmaf(-alpha, acc, p.keep * pre[i]) : alpha * acc);
         }
-        if (UPDATE && k == 0 && left > 32) orth_load_rows(w_src + (int64_t)32 * p.cols, p.cols, left - 32, pre);
+        if (UPDATE && BN == 256 && k == 0 && left > 32) orth_load_rows(w_src + (int64_t)32 * p.cols, p.cols, left - 32, pre);
         const int n_rows = col < p.cols ? left - 32 * k : 0;
         float *w_at = p.w + at + (int64_t)(32 * k) * p.cols + col;
         uint16_t *o_at = p.out16 + at + (int64_t)(32 * k) * p.cols + col;

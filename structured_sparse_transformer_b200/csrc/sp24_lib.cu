@@ -795,21 +795,29 @@ sp24_status launch_orth_products(const OrthMaps &maps, OrthProducts p, cudaStrea
   return SP24_OK;
 }
 
-template <bool BF16, bool UPDATE, bool TALL>
-sp24_status launch_orth_last_t(const CUtensorMap &p_rows, const CUtensorMap &x_cols, const OrthLast &p, cudaStream_t s) {
-  constexpr auto kernel = orth_last_kernel<BF16, UPDATE, TALL>;
+// x_cols: X in boxes of 64 columns x 64 rows; p_rows, p_half: P in boxes of 128 and 64 rows.
+struct OrthLastMaps {
+  CUtensorMap x_cols, p_rows, p_half;
+};
+
+template <bool BF16, bool UPDATE, bool TALL, int BN>
+sp24_status launch_orth_last_t(const OrthLastMaps &m, OrthLast p, cudaStream_t s) {
+  constexpr auto kernel = orth_last_kernel<BF16, UPDATE, TALL, BN>;
   const int pairs = pairs_of<kernel, kOlThreads, kOlSmem>();
   if (pairs <= 0) return pairs == 0 ? SP24_ERR_CUDA : SP24_ERR_NO_DEVICE;
+  p.tiles = (p.cols + 255) / 256 * ((p.rows + BN - 1) / BN);
   const int64_t tiles = (int64_t)p.batch * p.tiles;
   const int grid = (int)(tiles < pairs ? tiles : pairs);
-  return launch_pdl(kernel, dim3(2 * grid), dim3(kOlThreads), kOlSmem, s, TALL ? p_rows : x_cols, TALL ? x_cols : p_rows, p);
+  return launch_pdl(kernel, dim3(2 * grid), dim3(kOlThreads), kOlSmem, s, TALL ? m.p_rows : m.x_cols,
+                    TALL ? m.x_cols : (BN == 256 ? m.p_rows : m.p_half), p);
 }
 
+// Narrow tiles while all of them run at once (512 x 256: 11.4 us of the step with wide ones).
 template <bool BF16, bool UPDATE>
-sp24_status launch_orth_last(const CUtensorMap &p_rows, const CUtensorMap &x_cols, bool tall, const OrthLast &p,
-                             cudaStream_t s) {
-  return tall ? launch_orth_last_t<BF16, UPDATE, true>(p_rows, x_cols, p, s)
-              : launch_orth_last_t<BF16, UPDATE, false>(p_rows, x_cols, p, s);
+sp24_status launch_orth_last(const OrthLastMaps &m, bool tall, const OrthLast &p, cudaStream_t s) {
+  const bool narrow = 2 * (int64_t)p.batch * p.tiles <= sm_count() / 2;
+  if (narrow) return tall ? launch_orth_last_t<BF16, UPDATE, true, 128>(m, p, s) : launch_orth_last_t<BF16, UPDATE, false, 128>(m, p, s);
+  return tall ? launch_orth_last_t<BF16, UPDATE, true, 256>(m, p, s) : launch_orth_last_t<BF16, UPDATE, false, 256>(m, p, s);
 }
 
 sp24_status run_orth(const OrthPlan &pl, OrthSrc src, const OrthOut &o, int steps, float eps, void *workspace,
@@ -887,12 +895,10 @@ sp24_status run_orth(const OrthPlan &pl, OrthSrc src, const OrthOut &o, int step
   l.keep = o.keep;
   l.w = o.w;
   l.out16 = o.out16;
-  const CUtensorMap &x_cols = maps.x_half[(steps - 1) & 1];
-  if (o.bf16)
-    return o.w ? launch_orth_last<true, true>(maps.p_rows, x_cols, pl.tall, l, stream)
-               : launch_orth_last<true, false>(maps.p_rows, x_cols, pl.tall, l, stream);
-  return o.w ? launch_orth_last<false, true>(maps.p_rows, x_cols, pl.tall, l, stream)
-             : launch_orth_last<false, false>(maps.p_rows, x_cols, pl.tall, l, stream);
+  OrthLastMaps lm = {maps.x_half[(steps - 1) & 1], maps.p_rows, maps.p_rows};
+  if (!pl.tall && !make_map_3d(&lm.p_half, poly, m, m, bt, pm, m * pm, 64, 64, s128)) return SP24_ERR_CUDA;
+  if (o.bf16) return o.w ? launch_orth_last<true, true>(lm, pl.tall, l, stream) : launch_orth_last<true, false>(lm, pl.tall, l, stream);
+  return o.w ? launch_orth_last<false, true>(lm, pl.tall, l, stream) : launch_orth_last<false, false>(lm, pl.tall, l, stream);
 }
 
 sp24_status validate_orth(const OrthPlan &pl, int steps, float eps, const void *workspace, size_t workspace_bytes) {
