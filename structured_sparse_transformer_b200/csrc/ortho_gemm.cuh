@@ -580,6 +580,336 @@ __global__ void __launch_bounds__(kOgThreads, 1)
   }
 }
 
+// ------------------------------------------------------------------ short sides up to 256
+// G and P are one 256 x 256 tile then, so every CTA pair of a matrix's cluster computes them for
+// itself and keeps them in its shared memory: S holds 128 rows of G, then of P, per CTA in the
+// K-major operand layout, four blocks of 64 columns, which serves as both operands of G G^T
+// and as A of P X.  Gram takes X's rows as both operands too, so a stage is one 16 KB load.
+// Only P X is shared out (tiles of bn columns), and only X' passes through global memory:
+// one hand-over a round instead of three (512 x 256: 64 us of phases became 47).
+// With the last round's P stored by the first pair, orth_last_kernel follows as always.
+constexpr int kOsStages = 8;
+constexpr int kOsStageBytes = 128 * 128;
+constexpr int kOsSBytes = 4 * 128 * 128;
+constexpr int kOsStagingBytes = 2 * kOgTileBytes;      // per epilogue warp
+constexpr int kOsSmem = kOsStages * kOsStageBytes + kOsSBytes + kOgEpiWarps * kOsStagingBytes + kOgBarBytes + 1024;
+static_assert(kOsSmem <= 232448 && 8 * (2 * kOsStages + 8) <= kOgBarBytes, "shared memory per CTA");
+
+__global__ void __launch_bounds__(kOgThreads, 1)
+    orth_small_kernel(const __grid_constant__ OrthMaps maps, const __grid_constant__ CUtensorMap p_st128,
+                      const __grid_constant__ OrthProducts p) {
+  constexpr int kStages = kOsStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *s_mat = smem + kStages * kOsStageBytes;
+  uint8_t *epi_smem = s_mat + kOsSBytes;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(epi_smem + kOgEpiWarps * kOsStagingBytes);
+  uint64_t *full = bars;                       // [stages] leader: TMA (both CTAs) -> MMA
+  uint64_t *empty = bars + kStages;            // [stages] MMA -> this CTA's TMA
+  uint64_t *acc_full = bars + 2 * kStages;     // [2] MMA -> this CTA's epilogue
+  uint64_t *acc_empty = acc_full + 2;          // [2] leader: both epilogues -> MMA
+  uint64_t *drain = acc_empty + 2;
+  uint64_t *s_ready = drain + 1;               // leader: both epilogues have written S
+  uint64_t *round_done = s_ready + 1;          // the cluster's epilogue warps have finished the round
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(round_done + 1);
+  volatile int *s_abort = reinterpret_cast<volatile int *>(s_tmem + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t cta = cluster_ctarank();
+  const uint32_t rank = cta & 1;               // in the pair
+  const bool is_leader = rank == 0;
+  const uint16_t pair_mask = (uint16_t)(3u << (cta - rank));
+  const int pair = (int)cta >> 1, npairs = p.cluster >> 1;
+  const int b = (int)blockIdx.x / p.cluster;   // the matrix
+  const int rounds = (p.phases + 1) / 3;
+  const int kt_n = (p.n + 63) >> 6, kt_m = (p.m + 63) >> 6;
+  const int bn = p.bn[kOrthApply], tiles = p.tiles[kOrthApply];
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 2 * kOgEpiWarps);
+    }
+    mbar_init(drain, 1);
+    mbar_init(s_ready, 2 * kOgEpiWarps);
+    mbar_init(round_done, (uint32_t)(p.cluster * kOgEpiWarps));
+    *s_abort = 0;
+    fence_mbarrier_init();
+    prefetch_tensormap(&maps.x_rows[0]);
+    prefetch_tensormap(&maps.x_half[0]);
+    prefetch_tensormap(&maps.x_st[1]);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(s_tmem, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the cluster's barriers exist before any cross-CTA arrive or byte count
+  tc_fence_after();
+  const uint32_t tmem_base = *s_tmem;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------ producer (both CTAs)
+    uint32_t g = 0;
+    bool ok = true;
+    auto stage = [&](uint8_t *&st, uint64_t *&bar) {   // the next stage, once it is free
+      const int s = (int)(g % kStages);
+      ok = mbar_wait_bounded(&empty[s], ((g / kStages) & 1u) ^ 1u, p.wait_budget, s_abort);
+      if (!ok) return false;
+      st = smem + s * kOsStageBytes;
+      bar = &full[s];
+      if (is_leader) mbar_arrive_expect_tx(bar, 2 * 64 * 256);
+      ++g;
+      return true;
+    };
+    uint8_t *st;
+    uint64_t *bar;
+    for (int r = 0; ok && r < rounds; ++r) {
+      const int in = r & 1;
+      if (r > 0) {   // X of this round is written
+        if (!(ok = mbar_wait_cluster_bounded(round_done, (uint32_t)(r - 1) & 1u, p.wait_budget, s_abort))) break;
+        fence_proxy_async_all();
+      }
+      for (int kt = 0; kt < kt_n && stage(st, bar); ++kt)
+        tma_load_3d_pair(st, &maps.x_rows[in], bar, kt * 64, (int)rank * 128, b);
+      if (r + 1 == rounds) break;
+      for (int t = pair; ok && t < tiles; t += npairs) {
+        const int col = t * bn + (int)rank * (bn / 2);   // 64-column atoms of 64 rows; narrow tiles leave half a stage
+        for (int kt = 0; kt < kt_m && stage(st, bar); ++kt) {
+          tma_load_3d_pair(st, &maps.x_half[in], bar, col, kt * 64, b);
+          tma_load_3d_pair(st + 8192, &maps.x_half[in], bar, bn == 256 ? col + 64 : col, kt * 64, b);
+        }
+      }
+    }
+    // The leader's `full` barriers count both CTAs' bytes: let every copy land.
+    if (is_leader) {
+      for (uint32_t i = g > kStages ? g - kStages : 0; i < g; ++i) {
+        volatile int no_abort = 0;
+        mbar_wait_bounded(&full[i % kStages], (i / kStages) & 1u, kDrainBudget, &no_abort);
+      }
+    }
+  } else if (warp == 1 && lane == 0 && is_leader) {
+    // ----------------------------------------------------- MMA issuer (leader)
+    constexpr uint32_t idesc_sym = make_idesc_dense(false, 256, 256);
+    const uint32_t idesc_apply = make_idesc_dense(false, 256, bn) | (1u << 16);
+    const uint64_t st_desc = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+    const uint64_t st_desc_mn = smem_desc(smem_u32(smem), 8192, 1024, kSwizzle128B);
+    const uint64_t s_desc = smem_desc(smem_u32(s_mat), 16, 1024, kSwizzle128B);
+    uint32_t g = 0, n_ready = 0;
+    int j = 0;
+    bool ok = true;
+    auto acc_free = [&]() {
+      ok = mbar_wait_bounded(&acc_empty[j & 1], ((uint32_t)(j >> 1) & 1u) ^ 1u, p.wait_budget, s_abort);
+      tc_fence_after();
+      return ok;
+    };
+    auto loaded = [&](uint64_t &so) {
+      const int s = (int)(g % kStages);
+      ok = mbar_wait_bounded(&full[s], (g / kStages) & 1u, p.wait_budget, s_abort);
+      tc_fence_after();
+      so = (uint64_t)((s * kOsStageBytes) >> 4);
+      return ok;
+    };
+    auto s_written = [&]() {
+      ok = mbar_wait_cluster_bounded(s_ready, n_ready & 1u, p.wait_budget, s_abort);
+      ++n_ready;
+      tc_fence_after();
+      return ok;
+    };
+    uint64_t so;
+    for (int r = 0; ok && r < rounds; ++r) {
+      if (!acc_free()) break;   // Gram: a stage is both operands
+      for (int kt = 0; kt < kt_n && loaded(so); ++kt, ++g) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          tc_mma_f16_pair(tmem_base + (uint32_t)((j & 1) * 256), st_desc + so + 2 * kk, st_desc + so + 2 * kk, idesc_sym,
+                          (kt != 0 || kk != 0) ? 1u : 0u);
+        tc_commit_pair(&empty[g % kStages], pair_mask);
+      }
+      if (!ok) break;
+      tc_commit_pair(&acc_full[j & 1], pair_mask);
+      ++j;
+      if (!s_written() || !acc_free()) break;   // Poly: S is both operands
+      for (int kt = 0; kt < kt_m; ++kt)
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t at = s_desc + (uint64_t)(kt * (16384 >> 4) + 2 * kk);
+          tc_mma_f16_pair(tmem_base + (uint32_t)((j & 1) * 256), at, at, idesc_sym, (kt != 0 || kk != 0) ? 1u : 0u);
+        }
+      tc_commit_pair(&acc_full[j & 1], pair_mask);
+      ++j;
+      if (r + 1 == rounds) break;
+      if (!s_written()) break;
+      for (int t = pair; ok && t < tiles; t += npairs) {   // P X: A is S, B a stage of X, MN-major
+        if (!acc_free()) break;
+        for (int kt = 0; kt < kt_m && loaded(so); ++kt, ++g) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_f16_pair(tmem_base + (uint32_t)((j & 1) * 256), s_desc + (uint64_t)(kt * (16384 >> 4) + 2 * kk),
+                            st_desc_mn + so + (uint64_t)(kk * (2048 >> 4)), idesc_apply, (kt != 0 || kk != 0) ? 1u : 0u);
+          tc_commit_pair(&empty[g % kStages], pair_mask);
+        }
+        if (!ok) break;
+        tc_commit_pair(&acc_full[j & 1], pair_mask);
+        ++j;
+      }
+    }
+    if (!ok) {
+      tc_commit_pair(drain, (uint16_t)(1u << cta));
+      volatile int no_abort = 0;
+      mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
+    }
+  } else if (warp >= 2) {
+    // ---------------------------------------------------- epilogue (both CTAs)
+    // Warps, chunks and registers as in orth_products_kernel.
+    const int ew = warp - 2, grp = ew >> 2, q = warp & 3;
+    uint8_t *stg = epi_smem + ew * kOsStagingBytes;
+    const uint32_t stg_u32 = smem_u32(stg);
+    const int lr = lane >> 2, lc = 2 * (lane & 3);
+    const int d_row = 8 * ((lane >> 3) & 1) + (lane & 7), d_unit = lane >> 4;
+    const int row0 = (int)rank * 128 + 32 * q;   // of the matrix
+    const float gamma = __ldg(p.gamma + b);
+    // This lane's address of the 16 x 16 block (h, g) of chunk kk in S.
+    auto s_at = [&](int kk, int h, int g) {
+      return smem_u32(s_mat) + (uint32_t)((2 * grp + (kk >> 1)) * 16384) +
+             swz128(32 * q + 16 * h + d_row, 4 * (kk & 1) + 2 * g + d_unit);
+    };
+    bool alive = true;
+    int j = 0;
+    auto acc_here = [&]() {
+      const bool got = mbar_wait_bounded(&acc_full[j & 1], (uint32_t)(j >> 1) & 1u, p.wait_budget, s_abort);
+      alive = __all_sync(0xFFFFFFFFu, got);
+      tc_fence_after();
+      return alive;
+    };
+    auto release_acc = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_leader(&acc_empty[j & 1]);
+    };
+    for (int r = 0; alive && r < rounds; ++r) {
+      // G, then P, to S (entries past the matrix are zeros, but for a on P's diagonal, whose
+      // rows are clipped and whose columns meet X's zero rows).
+#pragma unroll 1
+      for (int poly = 0; poly < 2 && acc_here(); ++poly, ++j) {
+        const float alpha = r == 0 ? p.gram_alpha * gamma * gamma : p.gram_alpha;
+        const uint32_t t_base = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)((j & 1) * 256 + 128 * grp);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          uint32_t v[2][2][16];
+          orth_load_half(t_base + (uint32_t)(64 * half), 2, v);
+          if (half == 1) release_acc();
+          if (poly) {
+            const int diag = row0 + lr - (128 * grp + 64 * half + lc);   // row - column of the first entry
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                  uint32_t gv[4];
+                  ldmatrix_x4(s_at(2 * half + k, h, g), gv);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const int dd = diag + 16 * h + 8 * (e & 1) - 32 * k - 16 * g - 8 * (e >> 1);
+                    float gx, gy;
+                    unpack2<false>(gv[e], gx, gy);
+                    const float x = fmaf(p.c, __uint_as_float(v[k][h][8 * g + 2 * e]), p.b * gx) + (dd == 0 ? p.a : 0.0f);
+                    const float y = fmaf(p.c, __uint_as_float(v[k][h][8 * g + 2 * e + 1]), p.b * gy) + (dd == 1 ? p.a : 0.0f);
+                    v[k][h][4 * g + e] = pack2<false>(x, y);
+                  }
+                }
+            __syncwarp();   // every lane has its entries of G: P takes their places
+          } else {
+#pragma unroll
+            for (int kh = 0; kh < 4; ++kh)
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                v[kh >> 1][kh & 1][e] = pack2<false>(alpha * __uint_as_float(v[kh >> 1][kh & 1][2 * e]),
+                                                     alpha * __uint_as_float(v[kh >> 1][kh & 1][2 * e + 1]));
+          }
+#pragma unroll
+          for (int kh = 0; kh < 4; ++kh)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const uint32_t *a = &v[kh >> 1][kh & 1][4 * g];
+              const uint32_t pk[4] = {a[0], a[1], a[2], a[3]};
+              stmatrix_x4(s_at(2 * half + (kh >> 1), kh & 1, g), pk);
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (poly && r + 1 == rounds) {   // the last P goes to orth_last_kernel
+          if (lane == 0 && pair == 0 && row0 < p.m) {
+            for (int k = 0; k < 2; ++k)
+              if (128 * grp + 64 * k < p.m)
+                tma_store_3d(&p_st128, s_mat + (2 * grp + k) * 16384 + 32 * q * 128, 128 * grp + 64 * k, row0, b);
+            bulk_commit_group();
+          }
+        } else if (lane == 0) {
+          mbar_arrive_cluster(s_ready, cta - rank);
+        }
+      }
+      if (!alive || r + 1 == rounds) break;
+      for (int t = pair; t < tiles && acc_here(); t += npairs, ++j) {
+        const int n0 = t * bn + bn / 2 * grp, halves = bn / 128;
+        const int nch = min(2 * halves, (p.n - n0 + 31) >> 5);   // chunks inside the matrix (none: <= 0)
+        const float alpha = r == 0 ? gamma : 1.0f;
+        const uint32_t t_base = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)((j & 1) * 256 + bn / 2 * grp);
+#pragma unroll 1
+        for (int half = 0; half < halves; ++half) {
+          uint32_t v[2][2][16];
+          orth_load_half(t_base + (uint32_t)(64 * half), 2, v);
+          if (half == halves - 1) release_acc();
+          if (2 * half >= nch || row0 >= p.m) continue;
+#pragma unroll
+          for (int kh = 0; kh < 4; ++kh)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              v[kh >> 1][kh & 1][e] = pack2<false>(alpha * __uint_as_float(v[kh >> 1][kh & 1][2 * e]),
+                                                   alpha * __uint_as_float(v[kh >> 1][kh & 1][2 * e + 1]));
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
+#pragma unroll
+          for (int kh = 0; kh < 4; ++kh)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const uint32_t *a = &v[kh >> 1][kh & 1][4 * g];
+              const uint32_t pk[4] = {a[0], a[1], a[2], a[3]};
+              stmatrix_x4(stg_u32 + (uint32_t)((kh >> 1) * kOgTileBytes) + swz64(16 * (kh & 1) + d_row, 2 * g + d_unit), pk);
+            }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {   // the TMA unit clips rows and columns past the matrix
+            tma_store_3d(&maps.x_st[1 - (r & 1)], stg, n0 + 64 * half, row0, b);
+            if (2 * half + 1 < nch)
+              tma_store_3d(&maps.x_st[1 - (r & 1)], stg + kOgTileBytes, n0 + 64 * half + 32, row0, b);
+            bulk_commit_group();
+          }
+        }
+      }
+      if (!alive) break;
+      if (lane == 0) bulk_wait_group<0>();   // this warp's part of X' is written
+      __syncwarp();
+      if (lane < p.cluster) mbar_arrive_cluster(round_done, (uint32_t)lane);
+    }
+    if (lane == 0) bulk_wait_group<0>();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the cluster's MMAs, copies and arrivals into this CTA are over
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, kTmemCols);
+  }
+}
+
 // ------------------------------------------------------------------ the last product
 struct OrthLast {
   int rows, cols;            // the matrices; tall: X holds their transposes

@@ -714,19 +714,18 @@ double orth_plan_phases(OrthProducts *p, int batch, int64_t P, bool cluster, int
   return us;
 }
 
-// Clusters of C CTAs of the products kernel that fit at once (and its shared-memory opt-in).
-template <int C>
+// Clusters of C CTAs of a products kernel that fit at once (and its shared-memory opt-in).
+template <auto kernel, int SMEM, int C>
 int orth_clusters() {
   static PerDevice cache;
   const int dev = current_device();
   if (dev < 0) return -1;
-  constexpr auto kernel = orth_products_kernel<true>;
   std::call_once(cache.once[dev], [&] {
     int n = 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(C);
     cfg.blockDim = dim3(kOgThreads);
-    cfg.dynamicSmemBytes = kOgSmem;
+    cfg.dynamicSmemBytes = SMEM;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = C;
@@ -734,7 +733,7 @@ int orth_clusters() {
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kOgSmem) != cudaSuccess ||
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
@@ -744,7 +743,21 @@ int orth_clusters() {
   return cache.value[dev];
 }
 
-sp24_status launch_orth_products(const OrthMaps &maps, OrthProducts p, cudaStream_t stream) {
+template <auto kernel, int SMEM>
+int orth_clusters_of(int c) {
+  return c == 2 ? orth_clusters<kernel, SMEM, 2>() : (c == 4 ? orth_clusters<kernel, SMEM, 4>() : orth_clusters<kernel, SMEM, 8>());
+}
+
+// A round of orth_small_kernel with P X on `pairs` pairs: Gram on each pair, Poly, P X, hand-over.
+double orth_small_round(OrthProducts *p, int pairs) {
+  const int kt_n = (p->n + 63) / 64, kt_m = (p->m + 63) / 64;
+  p->bn[kOrthApply] = p->n > 128 * pairs ? 256 : 128;
+  p->tiles[kOrthApply] = (p->n + p->bn[kOrthApply] - 1) / p->bn[kOrthApply];
+  const int turns = (p->tiles[kOrthApply] + pairs - 1) / pairs;
+  return 2.6 + 0.30 * kt_n + 2.0 + 0.30 * kt_m + turns * (0.30 * kt_m + 0.3) + 1.8 + 2.0;
+}
+
+sp24_status launch_orth_products(const OrthMaps &maps, const CUtensorMap &p_st128, OrthProducts p, cudaStream_t stream) {
   int64_t P = pairs_of<orth_products_kernel<false>, kOgThreads, kOgSmem>();
   if (P <= 0) return P == 0 ? SP24_ERR_CUDA : SP24_ERR_NO_DEVICE;
   if (P > kOgMaxPairs) P = kOgMaxPairs;
@@ -758,29 +771,46 @@ sp24_status launch_orth_products(const OrthMaps &maps, OrthProducts p, cudaStrea
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  const int matrices = p.batch;
   int64_t grid = 0;
-  double least = orth_plan_phases(&p, p.batch, P, false, &grid);
+  double least = orth_plan_phases(&p, matrices, P, false, &grid);
   // A cluster per matrix, of as many pairs as its phases use, where that is expected to be faster.
   for (int c = 2; c <= 8; c *= 2) {
-    const int fit = c == 2 ? orth_clusters<2>() : (c == 4 ? orth_clusters<4>() : orth_clusters<8>());
+    const int fit = orth_clusters_of<orth_products_kernel<true>, kOgSmem>(c);
     if (fit <= 0) continue;
     OrthProducts q = p;
     int64_t use = 0;
-    const double us = orth_plan_phases(&q, 1, c / 2, true, &use) * (double)((p.batch + fit - 1) / fit);
+    const double us = orth_plan_phases(&q, 1, c / 2, true, &use) * (double)((matrices + fit - 1) / fit);
     if (us < least) {
       least = us;
       p = q;
       p.cluster = c;
     }
   }
+  // Short sides up to 256: G and P in every pair's shared memory.
+  bool small = false;
+  for (int c = 2; c <= 8 && p.m <= 256; c *= 2) {
+    const int fit = orth_clusters_of<orth_small_kernel, kOsSmem>(c);
+    if (fit <= 0) continue;
+    OrthProducts q = p;
+    const double us = orth_small_round(&q, c / 2) * (double)((matrices + fit - 1) / fit);
+    if (us < least) {
+      least = us;
+      p = q;
+      p.cluster = c;
+      small = true;
+    }
+  }
   cudaError_t err;
   if (p.cluster) {
-    cfg.gridDim = dim3((unsigned)(p.cluster * p.batch));
+    cfg.gridDim = dim3((unsigned)(p.cluster * matrices));
     attr[0].val.clusterDim.x = (unsigned)p.cluster;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     p.batch = 1;
-    err = cudaLaunchKernelEx(&cfg, orth_products_kernel<true>, maps, p);
+    if (small) cfg.dynamicSmemBytes = kOsSmem;
+    err = small ? cudaLaunchKernelEx(&cfg, orth_small_kernel, maps, p_st128, p)
+                : cudaLaunchKernelEx(&cfg, orth_products_kernel<true>, maps, p);
   } else {
     cfg.gridDim = dim3(2 * (unsigned)grid);
     attr[0].val.clusterDim.x = 2;
@@ -842,7 +872,12 @@ sp24_status run_orth(const OrthPlan &pl, OrthSrc src, const OrthOut &o, int step
        make_map_3d(&maps.g_st, gram, m, m, bt, pm, m * pm, 32, 32, s64) &&
        make_map_3d(&maps.p_rows, poly, m, m, bt, pm, m * pm, 64, 128, s128) &&
        make_map_3d(&maps.p_st, poly, m, m, bt, pm, m * pm, 32, 32, s64);
+  CUtensorMap p_st128 = maps.p_st;   // orth_small_kernel's last P: 64 columns x 32 rows
+  if (pl.m <= 256) ok = ok && make_map_3d(&p_st128, poly, m, m, bt, pm, m * pm, 64, 32, s128);
   if (!ok) return SP24_ERR_CUDA;
+  // (what can fail fails before the momentum is touched)
+  const int pairs = pairs_of<orth_products_kernel<false>, kOgThreads, kOgSmem>();
+  if (pairs <= 0) return pairs == 0 ? SP24_ERR_CUDA : SP24_ERR_NO_DEVICE;
 
   // Scale of the iterate: a power of two near sqrt(n) (ortho_gemm.cuh).
   int e = 0;
@@ -882,7 +917,7 @@ sp24_status run_orth(const OrthPlan &pl, OrthSrc src, const OrthOut &o, int step
   p.c = kNsC;
   p.part = reinterpret_cast<float *>(ws + pl.part);
   p.counters = counters;
-  if ((st = launch_orth_products(maps, p, stream)) != SP24_OK) return st;
+  if ((st = launch_orth_products(maps, p_st128, p, stream)) != SP24_OK) return st;
   OrthLast l = {};
   l.rows = (int)pl.rows;
   l.cols = (int)pl.cols;
