@@ -586,7 +586,8 @@ __global__ void __launch_bounds__(kOgThreads, 1)
 // K-major operand layout, four blocks of 64 columns, which serves as both operands of G G^T
 // and as A of P X.  Gram takes X's rows as both operands too, so a stage is one 16 KB load.
 // Only P X is shared out (tiles of bn columns), and only X' passes through global memory:
-// one hand-over a round instead of three (512 x 256: 64 us of phases became 47).
+// one hand-over a round instead of three (orthogonalising 256 x 512 took 77 us with a cluster's
+// phases, 64 this way; 64 x 64 50 and 39).
 // With the last round's P stored by the first pair, orth_last_kernel follows as always.
 constexpr int kOsStages = 8;
 constexpr int kOsStageBytes = 128 * 128;

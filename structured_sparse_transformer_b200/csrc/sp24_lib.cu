@@ -754,7 +754,7 @@ double orth_small_round(OrthProducts *p, int pairs) {
   p->bn[kOrthApply] = p->n > 128 * pairs ? 256 : 128;
   p->tiles[kOrthApply] = (p->n + p->bn[kOrthApply] - 1) / p->bn[kOrthApply];
   const int turns = (p->tiles[kOrthApply] + pairs - 1) / pairs;
-  return 2.6 + 0.30 * kt_n + 2.0 + 0.30 * kt_m + turns * (0.30 * kt_m + 0.3) + 1.8 + 2.0;
+  return 2.6 + 0.35 * kt_n + 2.0 + 0.30 * kt_m + turns * (0.30 * kt_m + 0.3) + 1.8 + 2.0;
 }
 
 sp24_status launch_orth_products(const OrthMaps &maps, const CUtensorMap &p_st128, OrthProducts p, cudaStream_t stream) {
@@ -794,7 +794,7 @@ sp24_status launch_orth_products(const OrthMaps &maps, const CUtensorMap &p_st12
     if (fit <= 0) continue;
     OrthProducts q = p;
     const double us = orth_small_round(&q, c / 2) * (double)((matrices + fit - 1) / fit);
-    if (us < least) {
+    if (us < least || (small && us <= least)) {   // (as good by the model: the larger cluster)
       least = us;
       p = q;
       p.cluster = c;
