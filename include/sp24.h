@@ -404,7 +404,8 @@ SP24_API sp24_status sp24_flip_rate(const uint8_t *idx_prev, const uint8_t *idx_
  *   G    device fp32, count matrices batch_stride elements apart, row-major
  *        with leading dimension ldg >= cols (as the weight gradients above)
  *   out  device dtype [count][rows][cols] contiguous, overwritten
- *   steps 1..16; eps >= 0
+ *   steps 1..16; eps finite, >= 0.  (A matrix whose norm is below about 1e-4 eps
+ *        starts so small that fp16 holds it with less than the accuracy below.)
  *   workspace  device, sp24_orthogonalize_size() bytes, 16-byte aligned; its
  *        contents do not matter and are not kept.  One call uses it at a time:
  *        calls that may overlap (streams, graphs replayed side by side) take
@@ -431,7 +432,8 @@ SP24_API sp24_status sp24_orthogonalize(const float *G, int64_t count, int64_t r
  *   U = grad + mu momentum (nesterov != 0), or momentum
  *   W <- (1 - lr weight_decay) W - lr scale NS(U);   W16 <- round(W)
  *   grad, momentum, W  device fp32 [count][rows][cols] contiguous (grad is only
- *        read: the output of sp24_gemm_wgrad_decay or sp24_masked_decay)
+ *        read: the output of sp24_gemm_wgrad_decay or sp24_masked_decay);
+ *        the momentum overlaps neither of the others
  *   W16  device dtype [count][rows][cols], or NULL
  * The update is added to W in the last product's epilogue, from its fp32
  * accumulator.  Hyperparameters are values of the call (a captured graph keeps

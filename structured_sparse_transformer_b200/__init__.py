@@ -498,6 +498,13 @@ def _out_code(t, name: str) -> int:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}") from None
 
 
+def _expect_rows(t, name, numel, cols):
+    """As _expect, for a 16-bit result: a flat buffer, or rows of `cols` entries."""
+    _expect(t, name, t.dtype, numel)
+    if t.dim() > 1 and t.shape[-1] != cols:
+        raise ValueError(f"{name}: expected rows of {cols} entries, got shape {tuple(t.shape)}")
+
+
 def sp24_orthogonalize_size(rows: int, cols: int, count: int = 1) -> int:
     """Workspace bytes of sp24_orthogonalize and sp24_muon_step for `count` [rows, cols] matrices."""
     out = ctypes.c_size_t(0)
@@ -516,7 +523,7 @@ def sp24_orthogonalize(G, out, workspace, steps: int = 5, eps: float = 1e-7, str
     _need_rowmajor(out, workspace)
     _expect(G, "G", torch.float32, count * R * C)
     code = _out_code(out, "out")
-    _expect(out, "out", out.dtype, count * R * C)
+    _expect_rows(out, "out", count * R * C, C)
     _expect(workspace, "workspace", torch.uint8, sp24_orthogonalize_size(R, C, count))
     device = _one_device(G, out, workspace)
     ld = G.stride(-2) if R > 1 else C
@@ -541,9 +548,11 @@ def sp24_muon_step(grad, momentum, W, W16, workspace, lr: float, mu: float = 0.9
             raise ValueError(f"{name}: expected shape {tuple(W.shape)}, got {tuple(t.shape)}")
     code = SP24_F16 if W16 is None else _out_code(W16, "W16")
     if W16 is not None:
-        _expect(W16, "W16", W16.dtype, count * R * C)
+        _expect_rows(W16, "W16", count * R * C, C)
     _expect(workspace, "workspace", torch.uint8, sp24_orthogonalize_size(R, C, count))
     device = _one_device(grad, momentum, W, W16, workspace)
+    if momentum.data_ptr() in (grad.data_ptr(), W.data_ptr()) and momentum.numel():
+        raise ValueError("momentum: shares the memory of grad or W")
     _call_on(device, "sp24_muon_step", stream, _ptr(grad), _ptr(momentum), _ptr(W), _ptr(W16), code, count, R, C,
              float(mu), int(bool(nesterov)), float(lr), float(weight_decay), float(scale), int(steps), float(eps),
              _ptr(workspace), workspace.numel())

@@ -9,6 +9,7 @@
 #include <string.h>
 
 #include <atomic>
+#include <cmath>
 #include <map>
 #include <mutex>
 #include <utility>
@@ -936,8 +937,14 @@ sp24_status run_orth(const OrthPlan &pl, OrthSrc src, const OrthOut &o, int step
   return o.w ? launch_orth_last<false, true>(lm, pl.tall, l, stream) : launch_orth_last<false, false>(lm, pl.tall, l, stream);
 }
 
+// Two ranges of this many bytes have one in common.
+bool overlap(const void *a, const void *b, size_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return (x < y ? y - x : x - y) < bytes;
+}
+
 sp24_status validate_orth(const OrthPlan &pl, int steps, float eps, const void *workspace, size_t workspace_bytes) {
-  if (steps < 1 || steps > 16 || !(eps >= 0.0f)) return SP24_ERR_INVALID_ARG;
+  if (steps < 1 || steps > 16 || !(eps >= 0.0f) || std::isinf(eps)) return SP24_ERR_INVALID_ARG;
   if (pl.count == 0 || pl.m == 0) return SP24_OK;
   if (!workspace) return SP24_ERR_INVALID_ARG;
   if (!aligned16(workspace)) return SP24_ERR_MISALIGNED;
@@ -1416,6 +1423,9 @@ sp24_status sp24_muon_step(const float *grad, float *momentum, float *W, void *W
     return SP24_ERR_MISALIGNED;
   if ((st = check_device()) != SP24_OK) return st;
   if (empty) return SP24_OK;
+  // The momentum is written while the gradient may have to be read once more.
+  const size_t bytes = (size_t)count * rows * cols * sizeof(float);
+  if (overlap(momentum, grad, bytes) || overlap(momentum, W, bytes)) return SP24_ERR_INVALID_ARG;
   OrthSrc src = {};
   src.g = grad;
   src.m = momentum;

@@ -364,3 +364,17 @@ def test_starts_of_unusual_sizes(shape, case):
     sp.sp24_orthogonalize(u.float().contiguous(), one, _workspace(g), steps=1)
     ref = torch.stack([_ns(x.float(), 1) for x in u3]).view(u.shape)
     assert _rel(one, ref) <= max(_tol(x.float(), torch.float16, 1) for x in u3)
+
+
+def test_momentum_that_shares_memory_is_refused():
+    g, w = _grad((64, 48), 1), _grad((64, 48), 2, 0.02)
+    ws = _workspace(g)
+    w0, g0 = w.clone(), g.clone()
+    both = torch.zeros(100, 48, device="cuda")
+    for args in ((g, g, w), (g, w, w)):
+        with pytest.raises(ValueError, match="momentum"):
+            sp.sp24_muon_step(*args, None, ws, lr=0.1)
+    with pytest.raises(RuntimeError, match="INVALID_ARG"):   # rows in common
+        sp.sp24_muon_step(both[:64], both[36:], w, None, ws, lr=0.1)
+    torch.cuda.synchronize()
+    assert torch.equal(w, w0) and torch.equal(g, g0) and not both.any()

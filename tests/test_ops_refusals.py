@@ -182,3 +182,19 @@ def test_tile_numbering_of_the_symmetric_products():
                 seen.add((i, t - R * i * (i + 1) // 2))
             want = {(i, j) for i in range(rb) for j in range(cb) if j * bn < (i + 1) * 256}
             assert seen == want and len(seen) == total
+
+
+@pytest.mark.parametrize("call,kw", [(_orth, dict(eps=float("inf"))), (_muon, dict(eps=float("inf")))])
+def test_an_infinite_eps_is_refused(call, kw):
+    assert call(**kw) == E["SP24_ERR_INVALID_ARG"]
+
+
+def test_results_of_other_rows_are_refused():
+    """Right in size, but of other rows: a transposed result would hold other entries.  (A flat buffer is taken.)"""
+    g, ws = torch.zeros(64, 32), torch.zeros(sp.sp24_orthogonalize_size(64, 32), dtype=torch.uint8)
+    for shape, why in (((32, 64), "rows of 32"), ((1, 32, 64), "rows of 32"), ((2048,), "CUDA"), ((1, 64, 32), "CUDA")):
+        o = torch.zeros(shape, dtype=torch.float16)
+        with pytest.raises(ValueError, match=why):
+            sp.sp24_orthogonalize(g, o, ws)
+        with pytest.raises(ValueError, match=why):
+            sp.sp24_muon_step(g, g.clone(), g.clone(), o, ws, lr=0.1)
