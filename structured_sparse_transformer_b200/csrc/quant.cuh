@@ -50,27 +50,35 @@ template <bool BF16, bool MASKED, int TPR, int NV>
 __global__ void __launch_bounds__(kQuantThreads)
     quantize_vec_kernel(const uint16_t *__restrict__ X, int64_t rows, int64_t cols, int64_t ldx,
                         const uint8_t *__restrict__ idx, int8_t *__restrict__ q, float *__restrict__ scale) {
+  // Patterns' bits in shared memory before the wait: a look-up is off the path from idx to the
+  // values then.
+  __shared__ uint16_t s_bits[MASKED ? 256 : 1];
+  if (MASKED) s_bits[threadIdx.x] = g_tables.bits[threadIdx.x];
   pdl_launch_dependents();
+  if (MASKED) __syncthreads();
   pdl_wait();
   constexpr int kRows = kQuantThreads / TPR;
   const int t = threadIdx.x % TPR;
   const int nvec = (int)(cols >> 3);
   for (int64_t r = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR; r < rows; r += (int64_t)gridDim.x * kRows) {
     const uint4 *x = reinterpret_cast<const uint4 *>(X + r * ldx);
+    uint32_t two[MASKED ? NV : 1];   // the patterns of each unit's two blocks
+    if (MASKED) {
+      const uint16_t *id = reinterpret_cast<const uint16_t *>(idx + (r >> 2) * (cols >> 2));
+#pragma unroll
+      for (int k = 0; k < NV; ++k) two[k] = t + k * TPR < nvec ? (uint32_t)__ldg(id + t + k * TPR) : 0u;
+    }
     uint4 v[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) v[k] = t + k * TPR < nvec ? __ldcs(x + t + k * TPR) : make_uint4(0u, 0u, 0u, 0u);
     if (MASKED) {
-      const uint16_t *id = reinterpret_cast<const uint16_t *>(idx + (r >> 2) * (cols >> 2));
       const int sh = 4 * (int)(r & 3);
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        if (t + k * TPR >= nvec) continue;
-        const uint32_t two = __ldg(id + t + k * TPR);
         uint32_t *e = reinterpret_cast<uint32_t *>(&v[k]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t keep = (uint32_t)g_tables.bits[(two >> (8 * h)) & 0xFFu] >> sh;
+          const uint32_t keep = (uint32_t)s_bits[(two[k] >> (8 * h)) & 0xFFu] >> sh;
           e[2 * h] &= ((keep & 1u) ? 0xFFFFu : 0u) | ((keep & 2u) ? 0xFFFF0000u : 0u);
           e[2 * h + 1] &= ((keep & 4u) ? 0xFFFFu : 0u) | ((keep & 8u) ? 0xFFFF0000u : 0u);
         }
