@@ -37,7 +37,6 @@ struct I8Geom {
   static constexpr int kStages = (232448 - kFixed) / kStageBytes < 8 ? (232448 - kFixed) / kStageBytes : 8;
   static constexpr int kSmem = kStages * kStageBytes + kFixed;
   static constexpr int kChunks = BN / 32;
-  static_assert(BN == 128 || BN == 256, "tile widths");
   static_assert(kStages >= 4 && 8 * (2 * kStages + 6) <= kI8BarBytes, "shared memory per CTA");
   static_assert(kStageBytes % 1024 == 0, "128B-swizzled tiles need 1 KB aligned starts");
 };
@@ -248,8 +247,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
 }
 
 // ------------------------------------------------------------------ few tokens
-// Where the 256-feature tiles above would leave most pairs idle (up to 128 tokens, or more with a
-// small weight): bound by reading Wq and by latency, so K is spread too.  A cluster of S CTAs
+// Where the 256-feature tiles above would leave most pairs idle and K is long: bound by reading Wq
+// and by latency, so K is spread too.  A cluster of S CTAs
 // (S = 1, 2, 4 or 8) computes 128 features x TP tokens, each CTA an S-th of K: M = 128, N = TP
 // MMAs (cta_group::1) on tiles that one thread loads as fast as the ring of stages takes them.  The 32-bit integer partial sums
 // meet through distributed shared memory: each CTA leaves its own in shared memory, and CTA r
@@ -322,40 +321,55 @@ __global__ void __launch_bounds__(kI8sThreads)
   pdl_wait();
 
   bool done = true;   // epilogue warps: the accumulator was there
-  if (warp == 0 && lane == 0) {
-    int g = 0;
-    bool ok = true;
+  if (warp == 0) {
+    int g = 0, s = 0;
+    uint32_t turn = 0;   // of the ring (counted: a division by `stages` costs as much as the rest of the loop)
     for (int kt = kb; kt < ke; ++kt, ++g) {
-      const int s = g % stages;
-      if (!(ok = mbar_wait_bounded(&empty[s], ((uint32_t)(g / stages) & 1u) ^ 1u, wait_budget, s_abort))) break;
-      uint8_t *st = smem + s * G::kStageBytes;
-      mbar_arrive_expect_tx(&full[s], G::kStageBytes);
-      tma_load_2d(st, &tm_w, &full[s], kt * 128, f0);
-      tma_load_2d(st + G::kSmemW, &tm_x, &full[s], kt * 128, t0);
+      const bool got = mbar_wait_bounded(&empty[s], turn ^ 1u, wait_budget, s_abort);
+      if (!__all_sync(0xFFFFFFFFu, got)) break;
+      if (elect_one()) {
+        uint8_t *st = smem + s * G::kStageBytes;
+        mbar_arrive_expect_tx(&full[s], G::kStageBytes);
+        tma_load_2d(st, &tm_w, &full[s], kt * 128, f0);
+        tma_load_2d(st + G::kSmemW, &tm_x, &full[s], kt * 128, t0);
+      }
+      __syncwarp();
+      if (++s == stages) {
+        s = 0;
+        turn ^= 1u;
+      }
     }
     for (int i = g > stages ? g - stages : 0; i < g; ++i) {   // every copy lands before the block ends
       volatile int no_abort = 0;
       mbar_wait_bounded(&full[i % stages], (uint32_t)(i / stages) & 1u, kDrainBudget, &no_abort);
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     constexpr uint32_t idesc = make_idesc_i8(128, TP);
     const uint64_t a_desc0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
     const uint64_t b_desc0 = smem_desc(smem_u32(smem + G::kSmemW), 16, 1024, kSwizzle128B);
-    int g = 0;
+    int s = 0;
+    uint32_t turn = 0;
     bool ok = true;
-    for (int kt = kb; kt < ke; ++kt, ++g) {
-      const int s = g % stages;
-      if (!(ok = mbar_wait_bounded(&full[s], (uint32_t)(g / stages) & 1u, wait_budget, s_abort))) break;
+    for (int kt = kb; kt < ke; ++kt) {
+      const bool got = mbar_wait_bounded(&full[s], turn, wait_budget, s_abort);
+      if (!(ok = __all_sync(0xFFFFFFFFu, got))) break;
       tc_fence_after();
       const uint64_t so = (uint64_t)((s * G::kStageBytes) >> 4);
+      if (elect_one()) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)   // 32 bytes along the 128-byte swizzled rows each
-        tc_mma_i8(tmem_base, a_desc0 + so + 2 * kk, b_desc0 + so + 2 * kk, idesc, (kt != kb || kk != 0) ? 1u : 0u);
-      tc_commit(&empty[s]);
+        for (int kk = 0; kk < 4; ++kk)   // 32 bytes along the 128-byte swizzled rows each
+          tc_mma_i8(tmem_base, a_desc0 + so + 2 * kk, b_desc0 + so + 2 * kk, idesc, (kt != kb || kk != 0) ? 1u : 0u);
+        tc_commit(&empty[s]);
+      }
+      __syncwarp();
+      if (++s == stages) {
+        s = 0;
+        turn ^= 1u;
+      }
     }
-    if (ok) tc_commit(acc_full);
-    else {
-      tc_commit(drain);
+    if (elect_one()) tc_commit(ok ? acc_full : drain);
+    __syncwarp();
+    if (!ok) {
       volatile int no_abort = 0;
       mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
     }
@@ -456,7 +470,7 @@ __global__ void __launch_bounds__(kI8sThreads)
 constexpr int kI8vThreads = 128;
 constexpr int kI8vRows = 4;
 
-template <int TT, bool BF16, bool GELU>
+template <int TT, int KB, bool BF16, bool GELU>
 __global__ void __launch_bounds__(kI8vThreads)
     gemv_i8_kernel(const int8_t *__restrict__ Xq, const float *__restrict__ sx, int T, int K,
                    const int8_t *__restrict__ Wq, const float *__restrict__ sw, int N, uint16_t *__restrict__ Y) {
@@ -468,18 +482,29 @@ __global__ void __launch_bounds__(kI8vThreads)
   const int4 *x = reinterpret_cast<const int4 *>(Xq);
   const int units = K >> 4;
   int acc[kI8vRows][TT] = {};
-#pragma unroll 4
-  for (int u = threadIdx.x; u < units; u += kI8vThreads) {
-    int4 wv[kI8vRows], xv[TT];
+  // KB units of a thread in flight at once, the last of them guarded one by one (a remainder loop
+  // would take K = 6400, 400 units, in turns of one load latency each: 12.4 us at N = 6400, T = 1,
+  // against 10.0).  One where a thread has no more (K <= 2048): twice the blocks fit an SM
+  // (1600 x 6400 at T = 2: 3.9 us against 5.0).
+  for (int u0 = threadIdx.x; u0 < units; u0 += KB * kI8vThreads) {
+    int4 wv[KB][kI8vRows], xv[KB][TT];
 #pragma unroll
-    for (int r = 0; r < kI8vRows; ++r) wv[r] = __ldcs(w + (int64_t)r * units + u);
+    for (int i = 0; i < KB; ++i) {
+      const int u = u0 + i * kI8vThreads;
+      const bool in = u < units;
 #pragma unroll
-    for (int t = 0; t < TT; ++t) xv[t] = __ldg(x + (int64_t)min(t, T - 1) * units + u);
+      for (int r = 0; r < kI8vRows; ++r) wv[i][r] = in ? __ldcs(w + (int64_t)r * units + u) : make_int4(0, 0, 0, 0);
 #pragma unroll
-    for (int r = 0; r < kI8vRows; ++r)
+      for (int t = 0; t < TT; ++t) xv[i][t] = in ? __ldg(x + (int64_t)min(t, T - 1) * units + u) : make_int4(0, 0, 0, 0);
+    }
 #pragma unroll
-      for (int t = 0; t < TT; ++t)
-        acc[r][t] = __dp4a(wv[r].x, xv[t].x, __dp4a(wv[r].y, xv[t].y, __dp4a(wv[r].z, xv[t].z, __dp4a(wv[r].w, xv[t].w, acc[r][t]))));
+    for (int i = 0; i < KB; ++i)
+#pragma unroll
+      for (int r = 0; r < kI8vRows; ++r)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+          acc[r][t] = __dp4a(wv[i][r].x, xv[i][t].x,
+                             __dp4a(wv[i][r].y, xv[i][t].y, __dp4a(wv[i][r].z, xv[i][t].z, __dp4a(wv[i][r].w, xv[i][t].w, acc[r][t]))));
   }
 #pragma unroll
   for (int r = 0; r < kI8vRows; ++r)

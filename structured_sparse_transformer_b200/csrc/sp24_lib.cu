@@ -976,6 +976,35 @@ sp24_status launch_i8_pair(const int8_t *Xq, int64_t T, int64_t K, const int8_t 
                     (int)((K + 127) / 128), (uint64_t)g_wait_budget.load(), sw, sx);
 }
 
+// Parts of K: doubled while the CTAs stay within one per SM and each keeps two stages.
+int i8_split(int64_t tiles, int64_t kt) {
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= sm_count() && kt >= 4 * split) split *= 2;
+  return split;
+}
+
+// Whether gemm_i8_few_kernel is expected to be faster than the pairs' 256 x 256 tiles, from fits of
+// both over 9-1024 tokens, 640-25600 features and K from 640 to 12800 with weights from memory (mean
+// errors 5% and 3%): microseconds of launch and epilogue, then of each stage of 128 along K, more
+// as more SMs read.  At 100 tokens: 6400 x 1600 7.5 on pairs, 10.0 here; 1600 x 6400 17.9 and 9.4.
+bool i8_few_pays(int64_t T, int64_t K, int64_t N) {
+  const int64_t tp = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+  const int64_t sms = sm_count(), kt = (K + 127) / 128;
+  const int64_t tiles = (N + 127) / 128 * ((T + tp - 1) / tp), wide = (N + 255) / 256 * ((T + 255) / 256);
+  if (T > 128 && tiles > sms) return false;
+  const int split = i8_split(tiles, kt);
+  const int64_t mine = (kt + split - 1) / split, ctas = tiles * split;
+  const int64_t smem = (mine < 8 ? mine : 8) * (16384 + 128 * tp) + 1280;
+  const int64_t at_once = sms * (2 * smem <= 232448 ? 2 : 1);
+  const double stages = (double)(mine * ((ctas + at_once - 1) / at_once));
+  const double few = 2.8 + 0.018 * (double)tp + (split > 1 ? 0.4 + 0.017 * (double)tp : 0.0) +
+                     stages * (0.09 + 0.275 * (double)(ctas < sms ? ctas : sms) / (double)sms);
+  const int64_t pairs = sms / 2, used = wide < pairs ? wide : pairs;
+  const double pair = 3.35 + 0.0044 * (double)(T < 256 ? T : 256) +
+                      (double)(kt * ((wide + pairs - 1) / pairs)) * (0.26 + 0.136 * (double)used / (double)pairs);
+  return few < pair;
+}
+
 template <int TP, bool BF16, bool GELU>
 sp24_status launch_i8_few(const int8_t *Xq, int64_t T, int64_t K, const int8_t *Wq, int64_t N, void *Y, const float *sx,
                           const float *sw, cudaStream_t s) {
@@ -995,10 +1024,8 @@ sp24_status launch_i8_few(const int8_t *Xq, int64_t T, int64_t K, const int8_t *
     if (!opt_in.value[dev]) cudaGetLastError();
   });
   if (!opt_in.value[dev]) return SP24_ERR_CUDA;
-  // Parts of K: doubled while the CTAs stay within one per SM and each keeps two stages.
   const int64_t ft = (N + 127) / 128, tt = (T + TP - 1) / TP, kt = (K + 127) / 128;
-  int split = 1;
-  while (split < 8 && ft * tt * split * 2 <= sm_count() && kt >= 4 * split) split *= 2;
+  const int split = i8_split(ft * tt, kt);
   const int64_t mine = (kt + split - 1) / split;
   const int stages = (int)(mine < G::kStagesMost ? mine : G::kStagesMost);
   cudaLaunchConfig_t cfg = {};
@@ -1026,24 +1053,27 @@ sp24_status launch_i8_few(const int8_t *Xq, int64_t T, int64_t K, const int8_t *
 template <bool BF16, bool GELU>
 sp24_status launch_i8(const int8_t *Xq, int64_t T, int64_t K, const int8_t *Wq, int64_t N, void *Y, const float *sx,
                       const float *sw, cudaStream_t s) {
-  if (T <= 8) {
+  // Dot products while one pass of short blocks covers them (cold weights): 4 x 1600 x 6400 5.0 us
+  // against 5.5 on tensor cores, 8 x 6400 x 6400 17 against 10.3.
+  if (T <= 2 ? N <= 8192 || K >= 1024 : T <= 8 && T * N * ((K + 2047) / 2048) <= 25600) {
     const dim3 grid((unsigned)(N / kI8vRows));
     uint16_t *y = static_cast<uint16_t *>(Y);
-    return T == 1   ? launch_pdl(gemv_i8_kernel<1, BF16, GELU>, grid, dim3(kI8vThreads), 0, s, Xq, sx, (int)T, (int)K, Wq, sw, (int)N, y)
-           : T == 2 ? launch_pdl(gemv_i8_kernel<2, BF16, GELU>, grid, dim3(kI8vThreads), 0, s, Xq, sx, (int)T, (int)K, Wq, sw, (int)N, y)
-           : T <= 4 ? launch_pdl(gemv_i8_kernel<4, BF16, GELU>, grid, dim3(kI8vThreads), 0, s, Xq, sx, (int)T, (int)K, Wq, sw, (int)N, y)
-                    : launch_pdl(gemv_i8_kernel<8, BF16, GELU>, grid, dim3(kI8vThreads), 0, s, Xq, sx, (int)T, (int)K, Wq, sw, (int)N, y);
+    auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(kI8vThreads), 0, s, Xq, sx, (int)T, (int)K, Wq, sw, (int)N, y); };
+    if (K <= 16 * kI8vThreads)
+      return T == 1   ? go(gemv_i8_kernel<1, 1, BF16, GELU>)
+             : T == 2 ? go(gemv_i8_kernel<2, 1, BF16, GELU>)
+             : T <= 4 ? go(gemv_i8_kernel<4, 1, BF16, GELU>)
+                      : go(gemv_i8_kernel<8, 1, BF16, GELU>);
+    return T == 1   ? go(gemv_i8_kernel<1, 2, BF16, GELU>)
+           : T == 2 ? go(gemv_i8_kernel<2, 2, BF16, GELU>)
+           : T <= 4 ? go(gemv_i8_kernel<4, 2, BF16, GELU>)
+                    : go(gemv_i8_kernel<8, 2, BF16, GELU>);
   }
+  if (!i8_few_pays(T, K, N)) return launch_i8_pair<256, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);
   if (T <= 16) return launch_i8_few<16, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);
   if (T <= 32) return launch_i8_few<32, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);
   if (T <= 64) return launch_i8_few<64, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);
-  // Tiles of 128 x 128 that fit the SMs at once: as long as the pairs' tiles would leave half of
-  // the pairs idle, splitting K pays (200 x 6400 x 1600: 18.6 us on 14 pairs).
-  if (T <= 128 || ((N + 127) / 128) * ((T + 127) / 128) <= sm_count())
-    return launch_i8_few<128, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);
-  if (((N + 255) / 256) * ((T + 255) / 256) >= sm_count() / 2)
-    return launch_i8_pair<256, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);
-  return launch_i8_pair<128, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);
+  return launch_i8_few<128, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);
 }
 
 // A warp per row holds the row in registers (up to 6144 entries); longer rows, and a matrix

@@ -113,6 +113,19 @@ __host__ __device__ constexpr uint32_t make_idesc_i8(int m, int n) {
 
 // ------------------------------------------------------------ waits and flags
 
+// True in one lane of a converged warp.  A loop that the whole warp runs, with the copies and MMAs
+// of a stage issued under this, keeps their descriptors in uniform registers; in a loop of one
+// lane alone each of them is moved there first (four MMAs and a commit take 300 cycles then).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t pred;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(pred));
+  return pred != 0;
+}
+
 // Wait until *flag >= target without sleeping (a phase's start waits on it).
 __device__ __forceinline__ bool flag_spin_bounded(const unsigned *flag, unsigned target, uint64_t budget,
                                                   volatile int *abort_flag) {

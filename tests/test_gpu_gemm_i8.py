@@ -172,8 +172,9 @@ def test_quantized_layer_stays_near_the_16_bit_one():
 
 
 def test_an_expired_wait_is_reported_and_the_next_call_is_right():
-    for T in (40, 700):
-        xq, sx, wq, sw = [t.cuda() for t in _operands(T, 1600, 528, 2)]
+    # (K long enough that no wait is over before it starts: 65536 in 64 or more steps)
+    for T, K in ((40, 65536), (3000, 65536)):
+        xq, sx, wq, sw = [t.cuda() for t in _operands(T, K, 528, 2)]
         want, y = (torch.empty(T, 528, dtype=torch.float16, device="cuda") for _ in range(2))
         sp.sp24_gemm_i8(xq, sx, wq, sw, want)
         try:
@@ -203,3 +204,17 @@ def test_outputs_past_32_bit_offsets():
         sp.sp24_gemm_i8(xq[lo:hi].contiguous(), sx[lo:hi].contiguous(), wq, sw, part)
         assert torch.equal(y[lo:hi], part)
     assert (y[T:] == 7.0).all() and sp.sp24_device_status() == 0
+
+
+@pytest.mark.parametrize("K,N", [(6400, 640), (4000, 1600), (3200, 3216), (9600, 6400)])
+@pytest.mark.parametrize("T", [1, 2, 3, 8, 12, 30, 60, 120, 300])
+def test_long_contractions_of_few_tokens(T, K, N):
+    """K in eight to one parts, every token tile; the last parts of K are shorter."""
+    _check(*_operands(T, K, N, T + K), "bf16", None)
+
+
+@pytest.mark.parametrize("K", [16, 2048, 2064, 6400])
+@pytest.mark.parametrize("T", [1, 2, 4, 5])
+def test_dot_products_of_odd_lengths(T, K):
+    """Units of 16 that end anywhere in a thread's turn."""
+    _check(*_operands(T, K, 400, T + K, full=True), "f16", "gelu")
