@@ -93,7 +93,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
   pdl_launch_dependents();
   pdl_wait();
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // ------------------------------------------------------ producer (both CTAs)
     uint32_t g = 0;
     bool ok = true;
@@ -101,14 +101,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       const int w_row = (tile % num_mt) * 256 + (int)rank * 128, x_row = (tile / num_mt) * BN + (int)rank * (BN / 2);
       for (int kt = 0; kt < num_kt; ++kt, ++g) {
         const int s = (int)(g % kStages);
-        if (!mbar_wait_bounded(&empty[s], ((g / kStages) & 1u) ^ 1u, wait_budget, s_abort)) {
-          ok = false;
-          break;
+        const bool got = mbar_wait_bounded(&empty[s], ((g / kStages) & 1u) ^ 1u, wait_budget, s_abort);
+        if (!(ok = __all_sync(0xFFFFFFFFu, got))) break;
+        if (elect_one()) {
+          uint8_t *st = smem + s * G::kStageBytes;
+          if (is_leader) mbar_arrive_expect_tx(&full[s], 2 * G::kStageBytes);
+          tma_load_2d_pair(st, &tm_w, &full[s], kt * 128, w_row);
+          tma_load_2d_pair(st + G::kSmemA, &tm_x, &full[s], kt * 128, x_row);
         }
-        uint8_t *st = smem + s * G::kStageBytes;
-        if (is_leader) mbar_arrive_expect_tx(&full[s], 2 * G::kStageBytes);
-        tma_load_2d_pair(st, &tm_w, &full[s], kt * 128, w_row);
-        tma_load_2d_pair(st + G::kSmemA, &tm_x, &full[s], kt * 128, x_row);
+        __syncwarp();
       }
     }
     // The leader's `full` barriers count both CTAs' bytes: let every copy land.
@@ -118,7 +119,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
         mbar_wait_bounded(&full[i % kStages], (i / kStages) & 1u, kDrainBudget, &no_abort);
       }
     }
-  } else if (warp == 1 && lane == 0 && is_leader) {
+  } else if (warp == 1 && is_leader) {
     // ----------------------------------------------------- MMA issuer (leader)
     constexpr uint32_t idesc = make_idesc_i8(256, BN);
     const uint64_t a_desc0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
@@ -128,23 +129,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
     int j = 0;
     for (int tile = pair; ok && tile < num_tiles; tile += npairs, ++j) {
       const int buf = j & 1;
-      if (!(ok = mbar_wait_bounded(&acc_empty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, wait_budget, s_abort))) break;
+      const bool freed = mbar_wait_bounded(&acc_empty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, wait_budget, s_abort);
+      if (!(ok = __all_sync(0xFFFFFFFFu, freed))) break;
       tc_fence_after();
       const uint32_t acc = tmem_base + (uint32_t)(buf * BN);
       for (int kt = 0; kt < num_kt; ++kt, ++g) {
         const int s = (int)(g % kStages);
-        if (!(ok = mbar_wait_bounded(&full[s], (g / kStages) & 1u, wait_budget, s_abort))) break;
+        const bool got = mbar_wait_bounded(&full[s], (g / kStages) & 1u, wait_budget, s_abort);
+        if (!(ok = __all_sync(0xFFFFFFFFu, got))) break;
         tc_fence_after();
         const uint64_t so = (uint64_t)((s * G::kStageBytes) >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)   // 32 bytes along the 128-byte swizzled rows each
-          tc_mma_i8_pair(acc, a_desc0 + so + 2 * kk, b_desc0 + so + 2 * kk, idesc, (kt != 0 || kk != 0) ? 1u : 0u);
-        tc_commit_pair(&empty[s], 0x3);
+          for (int kk = 0; kk < 4; ++kk)   // 32 bytes along the 128-byte swizzled rows each
+            tc_mma_i8_pair(acc, a_desc0 + so + 2 * kk, b_desc0 + so + 2 * kk, idesc, (kt != 0 || kk != 0) ? 1u : 0u);
+          tc_commit_pair(&empty[s], 0x3);
+          if (kt == num_kt - 1) tc_commit_pair(&acc_full[buf], 0x3);
+        }
+        __syncwarp();
       }
-      if (ok) tc_commit_pair(&acc_full[buf], 0x3);
     }
     if (!ok) {
-      tc_commit_pair(drain, 0x1);
+      if (elect_one()) tc_commit_pair(drain, 0x1);
+      __syncwarp();
       volatile int no_abort = 0;
       mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
     }

@@ -258,17 +258,15 @@ __global__ void __launch_bounds__(kOgThreads, 1)
       }
       if (!__all_sync(0xFFFFFFFFu, up)) break;
       __syncwarp();
-      if (lane == 0) {
-        fence_proxy_async_all();
-        mbar_arrive(ready);
-        while (ok && more) {
-          const int a_row = m0 + (int)rank * 128, b_row = n0 + (int)rank * (f.bn / 2);
-          for (int kt = kb; kt < ke; ++kt, ++g) {
-            const int s = (int)(g % kStages);
-            if (!mbar_wait_bounded(&empty[s], ((g / kStages) & 1u) ^ 1u, p.wait_budget, s_abort)) {
-              ok = false;
-              break;
-            }
+      fence_proxy_async_all();
+      if (lane == 0) mbar_arrive(ready);
+      while (ok && more) {
+        const int a_row = m0 + (int)rank * 128, b_row = n0 + (int)rank * (f.bn / 2);
+        for (int kt = kb; kt < ke; ++kt, ++g) {
+          const int s = (int)(g % kStages);
+          const bool got = mbar_wait_bounded(&empty[s], ((g / kStages) & 1u) ^ 1u, p.wait_budget, s_abort);
+          if (!(ok = __all_sync(0xFFFFFFFFu, got))) break;
+          if (elect_one()) {
             uint8_t *st = smem + s * kOgStageBytes;
             if (is_leader) mbar_arrive_expect_tx(&full[s], 2 * (16384 + 64 * f.bn));
             // K-major: rows of 64 entries along K; MN-major: 64-column atoms of 64 rows.
@@ -280,11 +278,11 @@ __global__ void __launch_bounds__(kOgThreads, 1)
               tma_load_3d_pair(st + 16384, mb, &full[s], kt * 64, b_row, b);
             }
           }
-          more = sched.next(tile, kb, ke);
-          if (more) orth_tile(p, f, b0, tile, b, m0, n0, below);
+          __syncwarp();
         }
+        more = sched.next(tile, kb, ke);
+        if (more) orth_tile(p, f, b0, tile, b, m0, n0, below);
       }
-      ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
     }
     // The leader's `full` barriers count both CTAs' bytes: let every copy land.
     if (is_leader && lane == 0) {
@@ -293,7 +291,7 @@ __global__ void __launch_bounds__(kOgThreads, 1)
         mbar_wait_bounded(&full[i % kStages], (i / kStages) & 1u, kDrainBudget, &no_abort);
       }
     }
-  } else if (warp == 1 && lane == 0 && is_leader) {
+  } else if (warp == 1 && is_leader) {
     // ----------------------------------------------------- MMA issuer (leader)
     uint32_t g = 0;
     bool ok = true;
@@ -310,25 +308,31 @@ __global__ void __launch_bounds__(kOgThreads, 1)
       int tile, kb, ke;
       for (; ok && sched.next(tile, kb, ke); ++j) {
         const int buf = j & 1;
-        if (!(ok = mbar_wait_bounded(&acc_empty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, p.wait_budget, s_abort))) break;
+        const bool freed = mbar_wait_bounded(&acc_empty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, p.wait_budget, s_abort);
+        if (!(ok = __all_sync(0xFFFFFFFFu, freed))) break;
         tc_fence_after();
         const uint32_t acc = tmem_base + (uint32_t)(buf * 256);
         for (int kt = kb; kt < ke; ++kt, ++g) {
           const int s = (int)(g % kStages);
-          if (!(ok = mbar_wait_bounded(&full[s], (g / kStages) & 1u, p.wait_budget, s_abort))) break;
+          const bool got = mbar_wait_bounded(&full[s], (g / kStages) & 1u, p.wait_budget, s_abort);
+          if (!(ok = __all_sync(0xFFFFFFFFu, got))) break;
           tc_fence_after();
           const uint64_t so = (uint64_t)((s * kOgStageBytes) >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_f16_pair(acc, a_desc0 + so + 2 * kk, b_desc0 + so + kk * b_step, idesc,
-                            (kt != kb || kk != 0) ? 1u : 0u);
-          tc_commit_pair(&empty[s], pair_mask);
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_f16_pair(acc, a_desc0 + so + 2 * kk, b_desc0 + so + kk * b_step, idesc,
+                              (kt != kb || kk != 0) ? 1u : 0u);
+            tc_commit_pair(&empty[s], pair_mask);
+            if (kt == ke - 1) tc_commit_pair(&acc_full[buf], pair_mask);
+          }
+          __syncwarp();
         }
-        if (ok) tc_commit_pair(&acc_full[buf], pair_mask);
       }
     }
     if (!ok) {
-      tc_commit_pair(drain, (uint16_t)(1u << cta));
+      if (elect_one()) tc_commit_pair(drain, (uint16_t)(1u << cta));
+      __syncwarp();
       volatile int no_abort = 0;
       mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
     }
@@ -656,47 +660,56 @@ __global__ void __launch_bounds__(kOgThreads, 1)
   pdl_launch_dependents();
   pdl_wait();
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // ------------------------------------------------------ producer (both CTAs)
     uint32_t g = 0;
     bool ok = true;
     auto stage = [&](uint8_t *&st, uint64_t *&bar) {   // the next stage, once it is free
       const int s = (int)(g % kStages);
-      ok = mbar_wait_bounded(&empty[s], ((g / kStages) & 1u) ^ 1u, p.wait_budget, s_abort);
-      if (!ok) return false;
+      const bool got = mbar_wait_bounded(&empty[s], ((g / kStages) & 1u) ^ 1u, p.wait_budget, s_abort);
+      ok = __all_sync(0xFFFFFFFFu, got);
       st = smem + s * kOsStageBytes;
       bar = &full[s];
-      if (is_leader) mbar_arrive_expect_tx(bar, 2 * 64 * 256);
-      ++g;
-      return true;
+      if (ok) ++g;
+      return ok;
     };
     uint8_t *st;
     uint64_t *bar;
     for (int r = 0; ok && r < rounds; ++r) {
       const int in = r & 1;
       if (r > 0) {   // X of this round is written
-        if (!(ok = mbar_wait_cluster_bounded(round_done, (uint32_t)(r - 1) & 1u, p.wait_budget, s_abort))) break;
+        const bool over = mbar_wait_cluster_bounded(round_done, (uint32_t)(r - 1) & 1u, p.wait_budget, s_abort);
+        if (!(ok = __all_sync(0xFFFFFFFFu, over))) break;
         fence_proxy_async_all();
       }
-      for (int kt = 0; kt < kt_n && stage(st, bar); ++kt)
-        tma_load_3d_pair(st, &maps.x_rows[in], bar, kt * 64, (int)rank * 128, b);
+      for (int kt = 0; kt < kt_n && stage(st, bar); ++kt) {
+        if (elect_one()) {
+          if (is_leader) mbar_arrive_expect_tx(bar, 2 * 64 * 256);
+          tma_load_3d_pair(st, &maps.x_rows[in], bar, kt * 64, (int)rank * 128, b);
+        }
+        __syncwarp();
+      }
       if (r + 1 == rounds) break;
       for (int t = pair; ok && t < tiles; t += npairs) {
         const int col = t * bn + (int)rank * (bn / 2);   // 64-column atoms of 64 rows; narrow tiles leave half a stage
         for (int kt = 0; kt < kt_m && stage(st, bar); ++kt) {
-          tma_load_3d_pair(st, &maps.x_half[in], bar, col, kt * 64, b);
-          tma_load_3d_pair(st + 8192, &maps.x_half[in], bar, bn == 256 ? col + 64 : col, kt * 64, b);
+          if (elect_one()) {
+            if (is_leader) mbar_arrive_expect_tx(bar, 2 * 64 * 256);
+            tma_load_3d_pair(st, &maps.x_half[in], bar, col, kt * 64, b);
+            tma_load_3d_pair(st + 8192, &maps.x_half[in], bar, bn == 256 ? col + 64 : col, kt * 64, b);
+          }
+          __syncwarp();
         }
       }
     }
     // The leader's `full` barriers count both CTAs' bytes: let every copy land.
-    if (is_leader) {
+    if (is_leader && lane == 0) {
       for (uint32_t i = g > kStages ? g - kStages : 0; i < g; ++i) {
         volatile int no_abort = 0;
         mbar_wait_bounded(&full[i % kStages], (i / kStages) & 1u, kDrainBudget, &no_abort);
       }
     }
-  } else if (warp == 1 && lane == 0 && is_leader) {
+  } else if (warp == 1 && is_leader) {
     // ----------------------------------------------------- MMA issuer (leader)
     constexpr uint32_t idesc_sym = make_idesc_dense(false, 256, 256);
     const uint32_t idesc_apply = make_idesc_dense(false, 256, bn) | (1u << 16);
@@ -707,19 +720,22 @@ __global__ void __launch_bounds__(kOgThreads, 1)
     int j = 0;
     bool ok = true;
     auto acc_free = [&]() {
-      ok = mbar_wait_bounded(&acc_empty[j & 1], ((uint32_t)(j >> 1) & 1u) ^ 1u, p.wait_budget, s_abort);
+      const bool got = mbar_wait_bounded(&acc_empty[j & 1], ((uint32_t)(j >> 1) & 1u) ^ 1u, p.wait_budget, s_abort);
+      ok = __all_sync(0xFFFFFFFFu, got);
       tc_fence_after();
       return ok;
     };
     auto loaded = [&](uint64_t &so) {
       const int s = (int)(g % kStages);
-      ok = mbar_wait_bounded(&full[s], (g / kStages) & 1u, p.wait_budget, s_abort);
+      const bool got = mbar_wait_bounded(&full[s], (g / kStages) & 1u, p.wait_budget, s_abort);
+      ok = __all_sync(0xFFFFFFFFu, got);
       tc_fence_after();
       so = (uint64_t)((s * kOsStageBytes) >> 4);
       return ok;
     };
     auto s_written = [&]() {
-      ok = mbar_wait_cluster_bounded(s_ready, n_ready & 1u, p.wait_budget, s_abort);
+      const bool got = mbar_wait_cluster_bounded(s_ready, n_ready & 1u, p.wait_budget, s_abort);
+      ok = __all_sync(0xFFFFFFFFu, got);
       ++n_ready;
       tc_fence_after();
       return ok;
@@ -728,42 +744,52 @@ __global__ void __launch_bounds__(kOgThreads, 1)
     for (int r = 0; ok && r < rounds; ++r) {
       if (!acc_free()) break;   // Gram: a stage is both operands
       for (int kt = 0; kt < kt_n && loaded(so); ++kt, ++g) {
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          tc_mma_f16_pair(tmem_base + (uint32_t)((j & 1) * 256), st_desc + so + 2 * kk, st_desc + so + 2 * kk, idesc_sym,
-                          (kt != 0 || kk != 0) ? 1u : 0u);
-        tc_commit_pair(&empty[g % kStages], pair_mask);
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_f16_pair(tmem_base + (uint32_t)((j & 1) * 256), st_desc + so + 2 * kk, st_desc + so + 2 * kk, idesc_sym,
+                            (kt != 0 || kk != 0) ? 1u : 0u);
+          tc_commit_pair(&empty[g % kStages], pair_mask);
+          if (kt == kt_n - 1) tc_commit_pair(&acc_full[j & 1], pair_mask);
+        }
+        __syncwarp();
       }
       if (!ok) break;
-      tc_commit_pair(&acc_full[j & 1], pair_mask);
       ++j;
       if (!s_written() || !acc_free()) break;   // Poly: S is both operands
-      for (int kt = 0; kt < kt_m; ++kt)
+      if (elect_one()) {
+        for (int kt = 0; kt < kt_m; ++kt)
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          const uint64_t at = s_desc + (uint64_t)(kt * (16384 >> 4) + 2 * kk);
-          tc_mma_f16_pair(tmem_base + (uint32_t)((j & 1) * 256), at, at, idesc_sym, (kt != 0 || kk != 0) ? 1u : 0u);
-        }
-      tc_commit_pair(&acc_full[j & 1], pair_mask);
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t at = s_desc + (uint64_t)(kt * (16384 >> 4) + 2 * kk);
+            tc_mma_f16_pair(tmem_base + (uint32_t)((j & 1) * 256), at, at, idesc_sym, (kt != 0 || kk != 0) ? 1u : 0u);
+          }
+        tc_commit_pair(&acc_full[j & 1], pair_mask);
+      }
+      __syncwarp();
       ++j;
       if (r + 1 == rounds) break;
       if (!s_written()) break;
       for (int t = pair; ok && t < tiles; t += npairs) {   // P X: A is S, B a stage of X, MN-major
         if (!acc_free()) break;
         for (int kt = 0; kt < kt_m && loaded(so); ++kt, ++g) {
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_f16_pair(tmem_base + (uint32_t)((j & 1) * 256), s_desc + (uint64_t)(kt * (16384 >> 4) + 2 * kk),
-                            st_desc_mn + so + (uint64_t)(kk * (2048 >> 4)), idesc_apply, (kt != 0 || kk != 0) ? 1u : 0u);
-          tc_commit_pair(&empty[g % kStages], pair_mask);
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_f16_pair(tmem_base + (uint32_t)((j & 1) * 256), s_desc + (uint64_t)(kt * (16384 >> 4) + 2 * kk),
+                              st_desc_mn + so + (uint64_t)(kk * (2048 >> 4)), idesc_apply, (kt != 0 || kk != 0) ? 1u : 0u);
+            tc_commit_pair(&empty[g % kStages], pair_mask);
+            if (kt == kt_m - 1) tc_commit_pair(&acc_full[j & 1], pair_mask);
+          }
+          __syncwarp();
         }
         if (!ok) break;
-        tc_commit_pair(&acc_full[j & 1], pair_mask);
         ++j;
       }
     }
     if (!ok) {
-      tc_commit_pair(drain, (uint16_t)(1u << cta));
+      if (elect_one()) tc_commit_pair(drain, (uint16_t)(1u << cta));
+      __syncwarp();
       volatile int no_abort = 0;
       mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
     }
@@ -996,7 +1022,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOlThreads, 1)
     m0 = (t % num_mt) * 256;
     n0 = (t / num_mt) * BN;
   };
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // ------------------------------------------------------ producer (both CTAs)
     uint32_t g = 0;
     bool ok = true;
@@ -1006,22 +1032,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOlThreads, 1)
       const int a_row = m0 + (int)rank * 128, b_row = n0 + (int)rank * (BN / 2);
       for (int kt = 0; kt < p.num_kt; ++kt, ++g) {
         const int s = (int)(g % kStages);
-        if (!mbar_wait_bounded(&empty[s], ((g / kStages) & 1u) ^ 1u, p.wait_budget, s_abort)) {
-          ok = false;
-          break;
+        const bool got = mbar_wait_bounded(&empty[s], ((g / kStages) & 1u) ^ 1u, p.wait_budget, s_abort);
+        if (!(ok = __all_sync(0xFFFFFFFFu, got))) break;
+        if (elect_one()) {
+          uint8_t *st = smem + s * kOgStageBytes;
+          if (is_leader) mbar_arrive_expect_tx(&full[s], 2 * (16384 + 64 * BN));
+          // P K-major, X in two 64-column atoms of 64 rows.
+          if (TALL) {
+            tma_load_3d_pair(st, &tm_a, &full[s], kt * 64, a_row, b);
+            tma_load_3d_pair(st + 16384, &tm_b, &full[s], b_row, kt * 64, b);
+            if (BN == 256) tma_load_3d_pair(st + 24576, &tm_b, &full[s], b_row + 64, kt * 64, b);
+          } else {
+            tma_load_3d_pair(st, &tm_a, &full[s], a_row, kt * 64, b);
+            tma_load_3d_pair(st + 8192, &tm_a, &full[s], a_row + 64, kt * 64, b);
+            tma_load_3d_pair(st + 16384, &tm_b, &full[s], kt * 64, b_row, b);
+          }
         }
-        uint8_t *st = smem + s * kOgStageBytes;
-        if (is_leader) mbar_arrive_expect_tx(&full[s], 2 * (16384 + 64 * BN));
-        // P K-major, X in two 64-column atoms of 64 rows.
-        if (TALL) {
-          tma_load_3d_pair(st, &tm_a, &full[s], kt * 64, a_row, b);
-          tma_load_3d_pair(st + 16384, &tm_b, &full[s], b_row, kt * 64, b);
-          if (BN == 256) tma_load_3d_pair(st + 24576, &tm_b, &full[s], b_row + 64, kt * 64, b);
-        } else {
-          tma_load_3d_pair(st, &tm_a, &full[s], a_row, kt * 64, b);
-          tma_load_3d_pair(st + 8192, &tm_a, &full[s], a_row + 64, kt * 64, b);
-          tma_load_3d_pair(st + 16384, &tm_b, &full[s], kt * 64, b_row, b);
-        }
+        __syncwarp();
       }
     }
     // The leader's `full` barriers count both CTAs' bytes: let every copy land.
@@ -1031,7 +1058,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOlThreads, 1)
         mbar_wait_bounded(&full[i % kStages], (i / kStages) & 1u, kDrainBudget, &no_abort);
       }
     }
-  } else if (warp == 1 && lane == 0 && is_leader) {
+  } else if (warp == 1 && is_leader) {
     // ----------------------------------------------------- MMA issuer (leader)
     constexpr uint32_t idesc = make_idesc_dense(false, 256, BN) | (TALL ? 1u << 16 : 1u << 15);
     const uint64_t a_desc0 = smem_desc(smem_u32(smem), TALL ? 16 : 8192, 1024, kSwizzle128B);
@@ -1041,25 +1068,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOlThreads, 1)
     int j = 0;
     for (int tile = pair; ok && tile < num_tiles; tile += npairs, ++j) {
       const int buf = j & 1;
-      if (!(ok = mbar_wait_bounded(&acc_empty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, p.wait_budget, s_abort))) break;
+      const bool freed = mbar_wait_bounded(&acc_empty[buf], ((uint32_t)(j >> 1) & 1u) ^ 1u, p.wait_budget, s_abort);
+      if (!(ok = __all_sync(0xFFFFFFFFu, freed))) break;
       tc_fence_after();
       const uint32_t acc = tmem_base + (uint32_t)(buf * 256);
       for (int kt = 0; kt < p.num_kt; ++kt, ++g) {
         const int s = (int)(g % kStages);
-        if (!(ok = mbar_wait_bounded(&full[s], (g / kStages) & 1u, p.wait_budget, s_abort))) break;
+        const bool got = mbar_wait_bounded(&full[s], (g / kStages) & 1u, p.wait_budget, s_abort);
+        if (!(ok = __all_sync(0xFFFFFFFFu, got))) break;
         tc_fence_after();
         const uint64_t so = (uint64_t)((s * kOgStageBytes) >> 4);
         // A K step of 16 moves 32 bytes along the rows, or, MN-major, 16 rows of 128 bytes.
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          tc_mma_f16_pair(acc, a_desc0 + so + kk * (TALL ? 2 : 2048 >> 4), b_desc0 + so + kk * (TALL ? 2048 >> 4 : 2),
-                          idesc, (kt != 0 || kk != 0) ? 1u : 0u);
-        tc_commit_pair(&empty[s], 0x3);
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_f16_pair(acc, a_desc0 + so + kk * (TALL ? 2 : 2048 >> 4), b_desc0 + so + kk * (TALL ? 2048 >> 4 : 2),
+                            idesc, (kt != 0 || kk != 0) ? 1u : 0u);
+          tc_commit_pair(&empty[s], 0x3);
+          if (kt == p.num_kt - 1) tc_commit_pair(&acc_full[buf], 0x3);
+        }
+        __syncwarp();
       }
-      if (ok) tc_commit_pair(&acc_full[buf], 0x3);
     }
     if (!ok) {
-      tc_commit_pair(drain, 0x1);
+      if (elect_one()) tc_commit_pair(drain, 0x1);
+      __syncwarp();
       volatile int no_abort = 0;
       mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
     }
