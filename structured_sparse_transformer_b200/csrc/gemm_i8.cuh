@@ -3,8 +3,8 @@
 //
 // A = Wq (feature = tensor-memory lane), B = Xq (token = accumulator column), both K-major in
 // rows of 128 bytes; exact 32-bit integer accumulation, then (float(acc) * sw[n]) * sx[t] in
-// fp32 and one rounding to the dtype.  A pair computes 256 features x BN tokens; each CTA
-// holds 128 rows of Wq and BN/2 rows of Xq per 128-deep stage, the pair's even CTA issues the
+// fp32 and one rounding to the dtype.  A pair computes 256 features x 256 tokens; each CTA
+// holds 128 rows of Wq and 128 rows of Xq per 128-deep stage, the pair's even CTA issues the
 // MMAs (K = 32 each).  Persistent over tiles, features fastest (the pairs running at once
 // share token tiles through L2), two accumulators, so a tile's epilogue overlaps the next
 // tile's main loop.
@@ -14,9 +14,9 @@
 // stmatrix.trans into a staging tile [32 tokens x 32 features] -> one TMA store.  Every wait
 // is bounded.
 //
-// Bound by the tensor cores: 32768 x 6400 x 1600 in 233-277 us (2.4-2.9 POP/s, by the box's power),
-// 2047 x 1024 x 4096 with GELU in 14.6 us (its epilogue's 4 us a tile against 3 us of stages).  At
-// 8192 tokens the tensor pipe is busy 64% of 66 us; DRAM reads are the operands once.
+// Bound by the tensor cores: 32768 x 6400 x 1600 in 227-277 us (2.4-3.0 POP/s, by the box's power),
+// 2047 x 1024 x 4096 with GELU in 14.4 us (its epilogue's 4 us a tile against 3 us of stages).  At
+// 8192 tokens the tensor pipe is busy 68% of 62 us; DRAM reads are the operands once.
 #pragma once
 #include "gemm_sp.cuh"
 #include "sp24_ops.cuh"
@@ -28,8 +28,8 @@ constexpr int kI8Threads = 64 + 32 * kI8EpiWarps;
 constexpr int kI8BarBytes = 512;
 constexpr int kI8TileBytes = 32 * 32 * 2;              // staging tile, 64B-swizzled
 
-template <int BN>
 struct I8Geom {
+  static constexpr int BN = 256;
   static constexpr int kSmemA = 128 * 128;
   static constexpr int kSmemB = (BN / 2) * 128;
   static constexpr int kStageBytes = kSmemA + kSmemB;
@@ -41,12 +41,13 @@ struct I8Geom {
   static_assert(kStageBytes % 1024 == 0, "128B-swizzled tiles need 1 KB aligned starts");
 };
 
-template <int BN, bool BF16, bool GELU>
+template <bool BF16, bool GELU>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
     gemm_i8_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                    const __grid_constant__ CUtensorMap tm_y, int N, int T, int num_kt, uint64_t wait_budget,
                    const float *__restrict__ sw, const float *__restrict__ sx) {
-  using G = I8Geom<BN>;
+  using G = I8Geom;
+  constexpr int BN = G::BN;
   constexpr int kStages = G::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -261,7 +262,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
 // meet through distributed shared memory: each CTA leaves its own in shared memory, and CTA r
 // adds all of them for tokens r, r + S, ..., scales and stores (integer sums: the order does
 // not matter).
-// At T = 1, K = 1600, N = 6400 the two-CTA tile above took 7.1 us with 25 CTA pairs reading.
+// At T = 37, K = 5120, N = 1280: 6.7 us, where the pairs' five tiles would take 15.
 constexpr int kI8sThreads = 64 + 256;                  // producer, MMA, eight epilogue warps
 constexpr int kI8sMaxStages = 8;
 

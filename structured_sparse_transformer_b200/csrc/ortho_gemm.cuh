@@ -13,7 +13,7 @@
 // the phase once its epilogue warps' stores are complete, and every TMA producer waits for the
 // count: only the producers stall, tensor memory, barriers and descriptors stay set up.
 // (As 15 launches, each phase paid for launch, set-up and drain: about 9 us each.)  At 1600 x 6400
-// this kernel's 14 phases take 329 us, 240 us of them stages at 0.36-0.40 us; the rest is the
+// this kernel's 14 phases take 302 us, 240 us of them stages at 0.36-0.40 us; the rest is the
 // exchange of split tiles and the hand-over between phases.
 // Small matrices (CLUSTER) take a cluster of CTA pairs each instead: they need not wait for one
 // another, no cooperative launch is needed, and the counts become arrivals on an mbarrier of

@@ -956,17 +956,18 @@ sp24_status validate_orth(const OrthPlan &pl, int steps, float eps, const void *
 // multiple of 16.
 constexpr int64_t kMaxI8K = 131056;
 
-template <int BN, bool BF16, bool GELU>
+template <bool BF16, bool GELU>
 sp24_status launch_i8_pair(const int8_t *Xq, int64_t T, int64_t K, const int8_t *Wq, int64_t N, void *Y,
                            const float *sx, const float *sw, cudaStream_t s) {
-  using G = I8Geom<BN>;
+  using G = I8Geom;
+  constexpr int BN = G::BN;
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   CUtensorMap tw, tx, ty;
   if (!make_map_2d(&tw, Wq, (uint64_t)K, (uint64_t)N, (uint64_t)K, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B, u8) ||
       !make_map_2d(&tx, Xq, (uint64_t)K, (uint64_t)T, (uint64_t)K, 128, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B, u8) ||
       !make_map_2d(&ty, Y, (uint64_t)N, (uint64_t)T, (uint64_t)N * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     return SP24_ERR_CUDA;
-  constexpr auto kernel = gemm_i8_kernel<BN, BF16, GELU>;
+  constexpr auto kernel = gemm_i8_kernel<BF16, GELU>;
   const int pairs = pairs_of<kernel, kI8Threads, G::kSmem>();
   if (pairs <= 0) return pairs == 0 ? SP24_ERR_CUDA : SP24_ERR_NO_DEVICE;
   const int64_t tiles = ((N + 255) / 256) * ((T + BN - 1) / BN);
@@ -986,7 +987,7 @@ int i8_split(int64_t tiles, int64_t kt) {
 // Whether gemm_i8_few_kernel is expected to be faster than the pairs' 256 x 256 tiles, from fits of
 // both over 9-1024 tokens, 640-25600 features and K from 640 to 12800 with weights from memory (mean
 // errors 5% and 3%): microseconds of launch and epilogue, then of each stage of 128 along K, more
-// as more SMs read.  At 100 tokens: 6400 x 1600 7.5 on pairs, 10.0 here; 1600 x 6400 17.9 and 9.4.
+// as more SMs read.  At 100 tokens: K 1600, N 6400 7.5 on pairs, 10.0 here; K 6400, N 1600 17.9 and 9.4.
 bool i8_few_pays(int64_t T, int64_t K, int64_t N) {
   const int64_t tp = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
   const int64_t sms = sm_count(), kt = (K + 127) / 128;
@@ -1069,7 +1070,7 @@ sp24_status launch_i8(const int8_t *Xq, int64_t T, int64_t K, const int8_t *Wq, 
            : T <= 4 ? go(gemv_i8_kernel<4, 2, BF16, GELU>)
                     : go(gemv_i8_kernel<8, 2, BF16, GELU>);
   }
-  if (!i8_few_pays(T, K, N)) return launch_i8_pair<256, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);
+  if (!i8_few_pays(T, K, N)) return launch_i8_pair<BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);
   if (T <= 16) return launch_i8_few<16, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);
   if (T <= 32) return launch_i8_few<32, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);
   if (T <= 64) return launch_i8_few<64, BF16, GELU>(Xq, T, K, Wq, N, Y, sx, sw, s);
