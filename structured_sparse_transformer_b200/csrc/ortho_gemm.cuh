@@ -555,17 +555,20 @@ __global__ void __launch_bounds__(kOgThreads, 1)
       }
       __syncwarp();
       if (lane == 0) bulk_wait_group<0>();   // this warp's stores of the phase are complete
-      if (!CLUSTER) {
-        named_barrier_sync(1, 32 * kOgEpiWarps);
-        if (ew == 0 && lane == 0 && alive) flag_add_release(p.counters + ph, 1u);
-      } else if (alive) {
-        // A warp without a tile comes here early: its arrival counts for this phase only once the
-        // one before is over, which the producer knows first (and must have seen before this
-        // phase can end: the barrier tells two phases apart, not three).
+      // No warp leaves a phase before its inputs were written (the producer acquired that for the CTA).
+      // One without a tile would run ahead otherwise: `ready` and `phase_done` tell two phases apart, not
+      // three, so its next wait for G would pass on the phase before last, and its arrival would
+      // count for a phase that is still open.
+      if (alive) {
         const bool up = mbar_wait_bounded(ready, (uint32_t)ph & 1u, p.wait_budget, s_abort);
         alive = __all_sync(0xFFFFFFFFu, up);
         __syncwarp();
-        if (alive && lane < p.cluster) mbar_arrive_cluster(phase_done, (uint32_t)lane);
+      }
+      if (!CLUSTER) {
+        named_barrier_sync(1, 32 * kOgEpiWarps);
+        if (ew == 0 && lane == 0 && alive) flag_add_release(p.counters + ph, 1u);
+      } else if (alive && lane < p.cluster) {
+        mbar_arrive_cluster(phase_done, (uint32_t)lane);
       }
     }
     if (lane == 0) {
