@@ -150,12 +150,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
         __syncwarp();
       }
     }
-    if (!ok) {
-      if (elect_one()) tc_commit_pair(drain, 0x1);
-      __syncwarp();
-      volatile int no_abort = 0;
-      mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
-    }
+    // The last MMAs are over before tensor and shared memory go, even if an epilogue gave up waiting for them.
+    if (elect_one()) tc_commit_pair(drain, 0x1);
+    __syncwarp();
+    volatile int no_abort = 0;
+    mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
   } else if (warp >= 2) {
     // ---------------------------------------------------- epilogue (both CTAs)
     // Warp w drains lanes 32q..32q+31 (q = w%4) at the 32-token chunks grp, grp + 4.  Register
@@ -247,6 +246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
 
   tc_fence_before();
   __syncthreads();
+  pair_abort_pause(s_abort);
   cluster_sync();  // the peer's MMAs, copies and arrivals into this CTA are over
   if (warp == 1) {
     tc_fence_after();
@@ -375,12 +375,12 @@ __global__ void __launch_bounds__(kI8sThreads)
         turn ^= 1u;
       }
     }
-    if (elect_one()) tc_commit(ok ? acc_full : drain);
+    uint64_t *over = ok ? acc_full : drain;
+    if (elect_one()) tc_commit(over);
     __syncwarp();
-    if (!ok) {
-      volatile int no_abort = 0;
-      mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
-    }
+    // The last MMAs are over before tensor and shared memory go, even if an epilogue gave up waiting for them.
+    volatile int no_abort = 0;
+    mbar_wait_bounded(over, 0, kDrainBudget, &no_abort);
   } else if (warp >= 2) {
     // This lane's feature of the tile; the two warps of a lane quadrant take tokens in turn.
     const int q = warp & 3, f = 32 * q + lane, turn = (warp - 2) >> 2;

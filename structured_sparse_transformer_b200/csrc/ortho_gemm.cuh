@@ -330,12 +330,11 @@ __global__ void __launch_bounds__(kOgThreads, 1)
         }
       }
     }
-    if (!ok) {
-      if (elect_one()) tc_commit_pair(drain, (uint16_t)(1u << cta));
-      __syncwarp();
-      volatile int no_abort = 0;
-      mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
-    }
+    // The last MMAs are over before tensor and shared memory go, even if an epilogue gave up waiting for them.
+    if (elect_one()) tc_commit_pair(drain, (uint16_t)(1u << cta));
+    __syncwarp();
+    volatile int no_abort = 0;
+    mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
   } else if (warp >= 2) {
     // ---------------------------------------------------- epilogue (both CTAs)
     // Warp w drains lanes 32q..32q+31 (q = w%4) at its half (grp) of the columns, four or two chunks
@@ -582,6 +581,7 @@ __global__ void __launch_bounds__(kOgThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  pair_abort_pause(s_abort);
   cluster_sync();  // the peer's MMAs, copies and arrivals into this CTA are over
   if (warp == 1) {
     tc_fence_after();
@@ -790,12 +790,11 @@ __global__ void __launch_bounds__(kOgThreads, 1)
         ++j;
       }
     }
-    if (!ok) {
-      if (elect_one()) tc_commit_pair(drain, (uint16_t)(1u << cta));
-      __syncwarp();
-      volatile int no_abort = 0;
-      mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
-    }
+    // The last MMAs are over before tensor and shared memory go, even if an epilogue gave up waiting for them.
+    if (elect_one()) tc_commit_pair(drain, (uint16_t)(1u << cta));
+    __syncwarp();
+    volatile int no_abort = 0;
+    mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
   } else if (warp >= 2) {
     // ---------------------------------------------------- epilogue (both CTAs)
     // Warps, chunks and registers as in orth_products_kernel.
@@ -935,6 +934,7 @@ __global__ void __launch_bounds__(kOgThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  pair_abort_pause(s_abort);
   cluster_sync();  // the cluster's MMAs, copies and arrivals into this CTA are over
   if (warp == 1) {
     tc_fence_after();
@@ -1093,12 +1093,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOlThreads, 1)
         __syncwarp();
       }
     }
-    if (!ok) {
-      if (elect_one()) tc_commit_pair(drain, 0x1);
-      __syncwarp();
-      volatile int no_abort = 0;
-      mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
-    }
+    // The last MMAs are over before tensor and shared memory go, even if an epilogue gave up waiting for them.
+    if (elect_one()) tc_commit_pair(drain, 0x1);
+    __syncwarp();
+    volatile int no_abort = 0;
+    mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
   } else if (warp >= 2) {
     // ---------------------------------------------------- epilogue (both CTAs)
     const int ew = warp - 2, grp = ew >> 2, q = warp & 3;
@@ -1158,6 +1157,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kOlThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  pair_abort_pause(s_abort);
   cluster_sync();  // the peer's MMAs, copies and arrivals into this CTA are over
   if (warp == 1) {
     tc_fence_after();
