@@ -209,6 +209,15 @@ static_assert(PairGeom<true, kEpiNone>::kMetaCol + 4 * PairGeom<true, kEpiNone>:
               "tensor memory budget");
 static_assert(2 * PairGeom<false, kEpiNone>::kStages + 16 + 2 * kEpiWarps <= kPairBarBytes / 8, "barrier space");
 
+// A CTA of a pair that gave up waiting stays for another millisecond (2^21 cycles).  Copies of both CTAs are counted
+// on the leader's barriers, and the leader waits for those it has armed; those that the other producer issued past
+// them are counted by nobody, and must land before their CTA ends.  They take microseconds.
+__device__ __forceinline__ void pair_abort_pause(const volatile int *abort_flag) {
+  if (!*abort_flag) return;
+  const long long t0 = clock64();
+  while (clock64() - t0 < (1ll << 21)) __nanosleep(1000);
+}
+
 // Work schedule of a CTA pair: a sequence of segments (tile, K steps kb..ke-1).
 // Data-parallel (every GEMM): pair p takes tiles p, p + P, p + 2P, ... over all
 // num_kt K steps, so the P pairs of a wave walk K in step and share each K
@@ -644,11 +653,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       }
       if (ok) tc_commit_pair(&acc_full[b], 0x3);
     }
-    if (!ok) {
-      tc_commit_pair(drain, 0x1);
-      volatile int no_abort = 0;
-      mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
-    }
+    // The last MMAs are over before tensor and shared memory go, even if an epilogue gave up waiting for them.
+    tc_commit_pair(drain, 0x1);
+    volatile int no_abort = 0;
+    mbar_wait_bounded(drain, 0, kDrainBudget, &no_abort);
   } else if (warp >= 2 && WG) {
     // ------------------------------------------ weight-gradient epilogue (both CTAs)
     // Warp w drains TMEM lanes 32q..32q+31 (q = w%4; rows of dW) at the 16-column
@@ -1056,6 +1064,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  pair_abort_pause(s_abort);
   cluster_sync();  // the peer's MMAs, copies and arrivals into this CTA are over
   if (warp == 1) {
     tc_fence_after();

@@ -90,15 +90,6 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
   }
 }
 
-// A CTA of a pair that gave up waiting stays for another millisecond (2^21 cycles).  Copies of both CTAs are counted
-// on the leader's barriers, and the leader waits for those it has armed; those that the other producer issued past
-// them are counted by nobody, and must land before their CTA ends.  They take microseconds.
-__device__ __forceinline__ void pair_abort_pause(const volatile int *abort_flag) {
-  if (!*abort_flag) return;
-  const long long t0 = clock64();
-  while (clock64() - t0 < (1ll << 21)) __nanosleep(1000);
-}
-
 // ------------------------------------------------ flags between CTAs (global)
 // Release increment of a counter in global memory (device scope): the
 // thread's earlier stores are visible to any thread whose acquire load sees it.

@@ -10,7 +10,7 @@ import pytest
 import structured_sparse_transformer_b200 as sp
 
 CSRC = os.path.join(os.path.dirname(os.path.abspath(sp.__file__)), "csrc")
-KERNELS = [("gemm_i8.cuh", "gemm_i8_kernel", True), ("gemm_i8.cuh", "gemm_i8_few_kernel", False),
+KERNELS = [("gemm_sp.cuh", "sp24_gemm_pair_kernel", True), ("gemm_i8.cuh", "gemm_i8_kernel", True), ("gemm_i8.cuh", "gemm_i8_few_kernel", False),
            ("ortho_gemm.cuh", "orth_products_kernel", True), ("ortho_gemm.cuh", "orth_small_kernel", True),
            ("ortho_gemm.cuh", "orth_last_kernel", True)]
 
