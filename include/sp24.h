@@ -438,7 +438,9 @@ SP24_API sp24_status sp24_orthogonalize(const float *G, int64_t count, int64_t r
  * The update is added to W in the last product's epilogue, from its fp32
  * accumulator.  Hyperparameters are values of the call (a captured graph keeps
  * them).  A NaN or infinity in U makes that weight NaN.  Sizes, steps, eps,
- * workspace and alignment as for sp24_orthogonalize.
+ * workspace and alignment as for sp24_orthogonalize.  Checks and set-up come
+ * before the first launch; if a launch itself fails (SP24_ERR_CUDA), the momentum
+ * may have been updated and W not.
  */
 SP24_API sp24_status sp24_muon_step(const float *grad, float *momentum, float *W, void *W16, sp24_dtype dtype,
                            int64_t count, int64_t rows, int64_t cols, float mu, int nesterov, float lr,

@@ -758,20 +758,19 @@ double orth_small_round(OrthProducts *p, int pairs) {
   return 2.6 + 0.35 * kt_n + 2.0 + 0.30 * kt_m + turns * (0.30 * kt_m + 0.3) + 1.8 + 2.0;
 }
 
-sp24_status launch_orth_products(const OrthMaps &maps, const CUtensorMap &p_st128, OrthProducts p, cudaStream_t stream) {
+// What orth_products_kernel or orth_small_kernel is launched with (and the kernels' set-up on this device).
+struct OrthProductsPlan {
+  OrthProducts p;
+  int matrices;
+  int64_t grid;   // pairs, without clusters per matrix
+  bool small;
+};
+
+sp24_status plan_orth_products(const OrthProducts &of, OrthProductsPlan *plan) {
+  OrthProducts p = of;
   int64_t P = pairs_of<orth_products_kernel<false>, kOgThreads, kOgSmem>();
   if (P <= 0) return P == 0 ? SP24_ERR_CUDA : SP24_ERR_NO_DEVICE;
   if (P > kOgMaxPairs) P = kOgMaxPairs;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kOgThreads);
-  cfg.dynamicSmemBytes = kOgSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
   const int matrices = p.batch;
   int64_t grid = 0;
   double least = orth_plan_phases(&p, matrices, P, false, &grid);
@@ -802,18 +801,34 @@ sp24_status launch_orth_products(const OrthMaps &maps, const CUtensorMap &p_st12
       small = true;
     }
   }
+  if (p.cluster) p.batch = 1;
+  *plan = {p, matrices, grid, small};
+  return SP24_OK;
+}
+
+sp24_status launch_orth_products(const OrthMaps &maps, const CUtensorMap &p_st128, const OrthProductsPlan &plan,
+                                 cudaStream_t stream) {
+  const OrthProducts &p = plan.p;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kOgThreads);
+  cfg.dynamicSmemBytes = plan.small ? kOsSmem : kOgSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   cudaError_t err;
   if (p.cluster) {
-    cfg.gridDim = dim3((unsigned)(p.cluster * matrices));
+    cfg.gridDim = dim3((unsigned)(p.cluster * plan.matrices));
     attr[0].val.clusterDim.x = (unsigned)p.cluster;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
-    p.batch = 1;
-    if (small) cfg.dynamicSmemBytes = kOsSmem;
-    err = small ? cudaLaunchKernelEx(&cfg, orth_small_kernel, maps, p_st128, p)
-                : cudaLaunchKernelEx(&cfg, orth_products_kernel<true>, maps, p);
+    err = plan.small ? cudaLaunchKernelEx(&cfg, orth_small_kernel, maps, p_st128, p)
+                     : cudaLaunchKernelEx(&cfg, orth_products_kernel<true>, maps, p);
   } else {
-    cfg.gridDim = dim3(2 * (unsigned)grid);
+    cfg.gridDim = dim3(2 * (unsigned)plan.grid);
     attr[0].val.clusterDim.x = 2;
     attr[1].id = cudaLaunchAttributeCooperative;   // its CTAs wait for one another: all are resident, or none starts
     attr[1].val.cooperative = 1;
@@ -831,11 +846,13 @@ struct OrthLastMaps {
   CUtensorMap x_cols, p_rows, p_half;
 };
 
+// launch false: the kernel's set-up on this device only.
 template <bool BF16, bool UPDATE, bool TALL, int BN>
-sp24_status launch_orth_last_t(const OrthLastMaps &m, OrthLast p, cudaStream_t s) {
+sp24_status orth_last_t(const OrthLastMaps &m, OrthLast p, cudaStream_t s, bool launch) {
   constexpr auto kernel = orth_last_kernel<BF16, UPDATE, TALL, BN>;
   const int pairs = pairs_of<kernel, kOlThreads, kOlSmem>();
   if (pairs <= 0) return pairs == 0 ? SP24_ERR_CUDA : SP24_ERR_NO_DEVICE;
+  if (!launch) return SP24_OK;
   p.tiles = (p.cols + 255) / 256 * ((p.rows + BN - 1) / BN);
   const int64_t tiles = (int64_t)p.batch * p.tiles;
   const int grid = (int)(tiles < pairs ? tiles : pairs);
@@ -845,10 +862,10 @@ sp24_status launch_orth_last_t(const OrthLastMaps &m, OrthLast p, cudaStream_t s
 
 // Narrow tiles while all of them run at once (512 x 256: 11.4 us of the step with wide ones).
 template <bool BF16, bool UPDATE>
-sp24_status launch_orth_last(const OrthLastMaps &m, bool tall, const OrthLast &p, cudaStream_t s) {
+sp24_status orth_last(const OrthLastMaps &m, bool tall, const OrthLast &p, cudaStream_t s, bool launch) {
   const bool narrow = 2 * (int64_t)p.batch * p.tiles <= sm_count() / 2;
-  if (narrow) return tall ? launch_orth_last_t<BF16, UPDATE, true, 128>(m, p, s) : launch_orth_last_t<BF16, UPDATE, false, 128>(m, p, s);
-  return tall ? launch_orth_last_t<BF16, UPDATE, true, 256>(m, p, s) : launch_orth_last_t<BF16, UPDATE, false, 256>(m, p, s);
+  if (narrow) return tall ? orth_last_t<BF16, UPDATE, true, 128>(m, p, s, launch) : orth_last_t<BF16, UPDATE, false, 128>(m, p, s, launch);
+  return tall ? orth_last_t<BF16, UPDATE, true, 256>(m, p, s, launch) : orth_last_t<BF16, UPDATE, false, 256>(m, p, s, launch);
 }
 
 sp24_status run_orth(const OrthPlan &pl, OrthSrc src, const OrthOut &o, int steps, float eps, void *workspace,
@@ -875,35 +892,14 @@ sp24_status run_orth(const OrthPlan &pl, OrthSrc src, const OrthOut &o, int step
        make_map_3d(&maps.p_st, poly, m, m, bt, pm, m * pm, 32, 32, s64);
   CUtensorMap p_st128 = maps.p_st;   // orth_small_kernel's last P: 64 columns x 32 rows
   if (pl.m <= 256) ok = ok && make_map_3d(&p_st128, poly, m, m, bt, pm, m * pm, 64, 32, s128);
+  OrthLastMaps lm = {maps.x_half[(steps - 1) & 1], maps.p_rows, maps.p_rows};
+  if (!pl.tall) ok = ok && make_map_3d(&lm.p_half, poly, m, m, bt, pm, m * pm, 64, 64, s128);
   if (!ok) return SP24_ERR_CUDA;
-  // (what can fail fails before the momentum is touched)
-  const int pairs = pairs_of<orth_products_kernel<false>, kOgThreads, kOgSmem>();
-  if (pairs <= 0) return pairs == 0 ? SP24_ERR_CUDA : SP24_ERR_NO_DEVICE;
 
   // Scale of the iterate: a power of two near sqrt(n) (ortho_gemm.cuh).
   int e = 0;
   while ((int64_t(1) << (2 * (e + 1))) <= pl.n) ++e;
   const float s = (float)(1 << e);
-
-  const int64_t col_tiles = (pl.cols + kOrthTile - 1) / kOrthTile;
-  const int64_t tiles = col_tiles * ((pl.rows + kOrthTile - 1) / kOrthTile);
-  int64_t blocks = (6 * (int64_t)sm_count() + pl.count - 1) / pl.count;   // six blocks of 256 threads an SM
-  if (blocks > tiles) blocks = tiles;
-  if (blocks > kOrthMaxBlocks) blocks = kOrthMaxBlocks;
-  const dim3 grid((unsigned)blocks, (unsigned)pl.count);
-  const bool quads = src.cols % 4 == 0 && src.ld % 4 == 0 && src.stride % 4 == 0 && aligned16(src.g) &&
-                     (!src.m || aligned16(src.m));
-  auto start = pl.tall ? (quads ? orth_start_kernel<true, true> : orth_start_kernel<true, false>)
-                       : (quads ? orth_start_kernel<false, true> : orth_start_kernel<false, false>);
-  sp24_status st = launch_pdl(start, grid, dim3(kOrthThreads), 0, stream, src, part, xb[0], pl.ldx, col_tiles, tiles);
-  if (st != SP24_OK) return st;
-  auto finish = pl.tall ? (quads ? orth_finish_start_kernel<true, true> : orth_finish_start_kernel<true, false>)
-                        : (quads ? orth_finish_start_kernel<false, true> : orth_finish_start_kernel<false, false>);
-  const int64_t few = (2 * (int64_t)sm_count() + pl.count - 1) / pl.count;
-  const dim3 grid2((unsigned)(blocks < few ? blocks : few), (unsigned)pl.count);
-  st = launch_pdl(finish, grid2, dim3(kOrthThreads), 0, stream, src, part, (int)blocks, s, eps, xb[0], pl.ldx, col_tiles,
-                  tiles, gamma, counters, kOgCounters);
-  if (st != SP24_OK) return st;
 
   OrthProducts p = {};
   p.m = (int)pl.m;
@@ -918,7 +914,6 @@ sp24_status run_orth(const OrthPlan &pl, OrthSrc src, const OrthOut &o, int step
   p.c = kNsC;
   p.part = reinterpret_cast<float *>(ws + pl.part);
   p.counters = counters;
-  if ((st = launch_orth_products(maps, p_st128, p, stream)) != SP24_OK) return st;
   OrthLast l = {};
   l.rows = (int)pl.rows;
   l.cols = (int)pl.cols;
@@ -931,10 +926,38 @@ sp24_status run_orth(const OrthPlan &pl, OrthSrc src, const OrthOut &o, int step
   l.keep = o.keep;
   l.w = o.w;
   l.out16 = o.out16;
-  OrthLastMaps lm = {maps.x_half[(steps - 1) & 1], maps.p_rows, maps.p_rows};
-  if (!pl.tall && !make_map_3d(&lm.p_half, poly, m, m, bt, pm, m * pm, 64, 64, s128)) return SP24_ERR_CUDA;
-  if (o.bf16) return o.w ? launch_orth_last<true, true>(lm, pl.tall, l, stream) : launch_orth_last<true, false>(lm, pl.tall, l, stream);
-  return o.w ? launch_orth_last<false, true>(lm, pl.tall, l, stream) : launch_orth_last<false, false>(lm, pl.tall, l, stream);
+  auto last = [&](bool launch) {
+    if (o.bf16) return o.w ? orth_last<true, true>(lm, pl.tall, l, stream, launch) : orth_last<true, false>(lm, pl.tall, l, stream, launch);
+    return o.w ? orth_last<false, true>(lm, pl.tall, l, stream, launch) : orth_last<false, false>(lm, pl.tall, l, stream, launch);
+  };
+  // Every kernel's set-up comes before the first launch, which advances the momentum: only a launch itself
+  // can fail after that.
+  OrthProductsPlan plan;
+  sp24_status st = plan_orth_products(p, &plan);
+  if (st != SP24_OK || (st = last(false)) != SP24_OK) return st;
+
+  const int64_t col_tiles = (pl.cols + kOrthTile - 1) / kOrthTile;
+  const int64_t tiles = col_tiles * ((pl.rows + kOrthTile - 1) / kOrthTile);
+  int64_t blocks = (6 * (int64_t)sm_count() + pl.count - 1) / pl.count;   // six blocks of 256 threads an SM
+  if (blocks > tiles) blocks = tiles;
+  if (blocks > kOrthMaxBlocks) blocks = kOrthMaxBlocks;
+  const dim3 grid((unsigned)blocks, (unsigned)pl.count);
+  const bool quads = src.cols % 4 == 0 && src.ld % 4 == 0 && src.stride % 4 == 0 && aligned16(src.g) &&
+                     (!src.m || aligned16(src.m));
+  auto start = pl.tall ? (quads ? orth_start_kernel<true, true> : orth_start_kernel<true, false>)
+                       : (quads ? orth_start_kernel<false, true> : orth_start_kernel<false, false>);
+  st = launch_pdl(start, grid, dim3(kOrthThreads), 0, stream, src, part, xb[0], pl.ldx, col_tiles, tiles);
+  if (st != SP24_OK) return st;
+  auto finish = pl.tall ? (quads ? orth_finish_start_kernel<true, true> : orth_finish_start_kernel<true, false>)
+                        : (quads ? orth_finish_start_kernel<false, true> : orth_finish_start_kernel<false, false>);
+  const int64_t few = (2 * (int64_t)sm_count() + pl.count - 1) / pl.count;
+  const dim3 grid2((unsigned)(blocks < few ? blocks : few), (unsigned)pl.count);
+  st = launch_pdl(finish, grid2, dim3(kOrthThreads), 0, stream, src, part, (int)blocks, s, eps, xb[0], pl.ldx, col_tiles,
+                  tiles, gamma, counters, kOgCounters);
+  if (st != SP24_OK) return st;
+
+  if ((st = launch_orth_products(maps, p_st128, plan, stream)) != SP24_OK) return st;
+  return last(true);
 }
 
 // Two ranges of this many bytes have one in common.

@@ -156,3 +156,18 @@ def test_g_is_read_after_it_is_written_on_a_planned_grid():
 
 def test_the_model_finds_the_fault_without_the_wait():
     assert any(_run(CASES[0], 14, False, seed) for seed in range(300))
+
+
+def test_set_up_comes_before_the_first_launch():
+    """What can fail without a launch (tensor maps, a kernel's set-up on its device) does so before the first kernel
+    advances the momentum: a refused step leaves every buffer as it was."""
+    text = open(os.path.join(CSRC, "sp24_lib.cu")).read()
+    run = text[text.index("sp24_status run_orth("):]
+    run = run[:run.index("\n}\n")]
+    behind = run[run.index("launch_pdl("):]
+    for what in ("make_map_", "pairs_of<", "orth_clusters", "plan_orth_products(", "last(false)"):
+        assert what not in behind, what
+    assert run.index("plan_orth_products(") < run.index("last(false)") < run.index("launch_pdl(")
+    launch = text[text.index("sp24_status launch_orth_products("):]
+    launch = launch[:launch.index("\n}\n")]
+    assert "pairs_of" not in launch and "orth_clusters" not in launch
