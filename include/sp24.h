@@ -66,7 +66,7 @@ typedef enum sp24_status {
   SP24_ERR_INVALID_ARG = 1,       /* null pointer, negative size, bad enum, ld < width */
   SP24_ERR_UNSUPPORTED_SHAPE = 2, /* a size is not a multiple the call needs */
   SP24_ERR_UNSUPPORTED_DTYPE = 3,
-  SP24_ERR_MISALIGNED = 4,        /* a pointer or row pitch is not 16-byte aligned */
+  SP24_ERR_MISALIGNED = 4,        /* a pointer or row pitch is not aligned as the call needs */
   SP24_ERR_CUDA = 5,              /* a CUDA runtime/driver call or launch failed */
   SP24_ERR_TIMEOUT = 6,           /* a kernel gave up waiting (see sp24_device_status) */
   SP24_ERR_NO_DEVICE = 7,         /* no sm_100 device is current */
@@ -458,7 +458,7 @@ SP24_API sp24_status sp24_muon_step(const float *grad, float *momentum, float *W
  *   idx    device uint8 [rows/4][cols/4] (sp24_mask_search; rows, cols multiples
  *          of 4), or NULL
  *   q      device int8 [rows x cols] contiguous, 16-byte aligned
- *   scale  device fp32 [rows]
+ *   scale  device fp32 [rows], 4-byte aligned
  * A row of zeros, or one whose amax is below 2^-100, gives scale 0 and q 0; a row
  * with a NaN or infinity (in a kept place) gives scale NaN and q 0.  rows,
  * cols >= 0 (cols == 0: scales of 0).
@@ -479,7 +479,7 @@ SP24_API sp24_status sp24_quantize_rows(const void *X, sp24_dtype dtype, int64_t
  *   epi SP24_EPI_NONE or SP24_EPI_GELU (no aux here: nothing is saved for a
  *       backward pass)
  * All row-major and contiguous.  K % 16 == 0, N % 16 == 0, K <= 131056 (where the
- * sum cannot overflow), T >= 0.  Xq, Wq and Y 16-byte aligned.
+ * sum cannot overflow), T >= 0.  Xq, Wq and Y 16-byte aligned, sx and sw 4-byte.
  */
 SP24_API sp24_status sp24_gemm_i8(const int8_t *Xq, const float *sx, int64_t T, int64_t K, const int8_t *Wq,
                          const float *sw, int64_t N, sp24_dtype dtype, void *Y, sp24_epilogue epi, void *stream);

@@ -1504,7 +1504,7 @@ sp24_status sp24_quantize_rows(const void *X, sp24_dtype dtype, int64_t rows, in
   if (!valid_dtype(dtype)) return SP24_ERR_UNSUPPORTED_DTYPE;
   if (idx && (rows % 4 || cols % 4)) return SP24_ERR_UNSUPPORTED_SHAPE;
   if (rows > 0 && (!scale || (cols > 0 && (!X || !q)))) return SP24_ERR_INVALID_ARG;
-  if (rows > 0 && cols > 0 && (!aligned16(X) || !aligned16(q))) return SP24_ERR_MISALIGNED;
+  if (rows > 0 && (!aligned_to(scale, 4) || (cols > 0 && (!aligned16(X) || !aligned16(q))))) return SP24_ERR_MISALIGNED;
   sp24_status st = check_device();
   if (st != SP24_OK) return st;
   if (rows == 0) return SP24_OK;
@@ -1520,7 +1520,7 @@ sp24_status sp24_gemm_i8(const int8_t *Xq, const float *sx, int64_t T, int64_t K
   if (!valid_dtype(dtype)) return SP24_ERR_UNSUPPORTED_DTYPE;
   if (epi != SP24_EPI_NONE && epi != SP24_EPI_GELU) return SP24_ERR_INVALID_ARG;
   if (K % 16 || N % 16 || K > kMaxI8K || T > INT32_MAX - 256 || N > INT32_MAX - 256) return SP24_ERR_UNSUPPORTED_SHAPE;
-  if (!aligned16(Xq) || !aligned16(Wq) || !aligned16(Y)) return SP24_ERR_MISALIGNED;
+  if (!aligned16(Xq) || !aligned16(Wq) || !aligned16(Y) || !aligned_to(sx, 4) || !aligned_to(sw, 4)) return SP24_ERR_MISALIGNED;
   sp24_status st = check_device();
   if (st != SP24_OK) return st;
   if (T == 0) return SP24_OK;

@@ -1,0 +1,40 @@
+"""More argument checks of the optimiser-step and 8-bit entry points (no device needed)."""
+import ctypes
+
+import pytest
+import torch
+
+import structured_sparse_transformer_b200 as sp
+
+E = {v: k for k, v in sp.STATUS.items()}
+F = ctypes.c_float
+A = [ctypes.c_void_p(0x10000000 * (k + 1)) for k in range(6)]      # far from one another
+
+
+def _raw(name, *args):
+    return getattr(sp.lib(), name)(*args)
+
+
+def _off(p, by):
+    return ctypes.c_void_p(p.value + by)
+
+
+def _i8(x=A[0], sx=A[1], T=32, K=64, w=A[2], sw=A[3], N=64, y=A[4]):
+    return _raw("sp24_gemm_i8", x, sx, T, K, w, sw, N, 0, y, 0, None)
+
+
+def _quant(x=A[0], rows=32, cols=64, ldx=64, idx=None, q=A[1], scale=A[2]):
+    return _raw("sp24_quantize_rows", x, 0, rows, cols, ldx, idx, q, scale, None)
+
+
+@pytest.mark.parametrize("by", [1, 2, 3])
+def test_scales_at_odd_addresses_are_refused(by):
+    """A 4-byte access at such an address would fault."""
+    assert _i8(sx=_off(A[1], by)) == _i8(sw=_off(A[3], by)) == E["SP24_ERR_MISALIGNED"]
+    assert _quant(scale=_off(A[2], by)) == _quant(cols=0, ldx=0, scale=_off(A[2], by)) == E["SP24_ERR_MISALIGNED"]
+
+
+def test_scales_at_word_addresses_are_taken():
+    if torch.cuda.is_available():
+        pytest.skip("a device is present")
+    assert _i8(sx=_off(A[1], 4), sw=_off(A[3], 8)) == _quant(scale=_off(A[2], 12)) == E["SP24_ERR_NO_DEVICE"]
