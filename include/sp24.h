@@ -418,6 +418,7 @@ SP24_API sp24_status sp24_flip_rate(const uint8_t *idx_prev, const uint8_t *idx_
  * large singular directions do not dwarf the others (the error grows in
  * proportion to |G|_2 over the typical entry of the rest).
  * G and out need only their types' alignment (a matrix of a stack of any size).
+ * The workspace overlaps neither of them (refused).
  */
 SP24_API sp24_status sp24_orthogonalize_size(int64_t count, int64_t rows, int64_t cols, size_t *workspace_bytes);
 SP24_API sp24_status sp24_orthogonalize(const float *G, int64_t count, int64_t rows, int64_t cols, int64_t ldg,
@@ -434,7 +435,8 @@ SP24_API sp24_status sp24_orthogonalize(const float *G, int64_t count, int64_t r
  *   grad, momentum, W  device fp32 [count][rows][cols] contiguous (grad is only
  *        read: the output of sp24_gemm_wgrad_decay or sp24_masked_decay);
  *        the momentum overlaps neither of the others
- *   W16  device dtype [count][rows][cols], or NULL
+ *   W16  device dtype [count][rows][cols], or NULL; overlaps none of the three,
+ *        nor does the workspace any buffer (all of this is refused)
  * The update is added to W in the last product's epilogue, from its fp32
  * accumulator.  Hyperparameters are values of the call (a captured graph keeps
  * them).  A NaN or infinity in U makes that weight NaN.  Sizes, steps, eps,
@@ -461,7 +463,8 @@ SP24_API sp24_status sp24_muon_step(const float *grad, float *momentum, float *W
  *   scale  device fp32 [rows], 4-byte aligned
  * A row of zeros, or one whose amax is below 2^-100, gives scale 0 and q 0; a row
  * with a NaN or infinity (in a kept place) gives scale NaN and q 0.  rows,
- * cols >= 0 (cols == 0: scales of 0).
+ * cols >= 0 (cols == 0: scales of 0).  q and scale overlap no other buffer (refused;
+ * of a pitched X, what lies between its rows counts as its own).
  */
 SP24_API sp24_status sp24_quantize_rows(const void *X, sp24_dtype dtype, int64_t rows, int64_t cols, int64_t ldx,
                                const uint8_t *idx, int8_t *q, float *scale, void *stream);
@@ -480,6 +483,7 @@ SP24_API sp24_status sp24_quantize_rows(const void *X, sp24_dtype dtype, int64_t
  *       backward pass)
  * All row-major and contiguous.  K % 16 == 0, N % 16 == 0, K <= 131056 (where the
  * sum cannot overflow), T >= 0.  Xq, Wq and Y 16-byte aligned, sx and sw 4-byte.
+ * Y overlaps no operand (refused).
  */
 SP24_API sp24_status sp24_gemm_i8(const int8_t *Xq, const float *sx, int64_t T, int64_t K, const int8_t *Wq,
                          const float *sw, int64_t N, sp24_dtype dtype, void *Y, sp24_epilogue epi, void *stream);

@@ -960,10 +960,22 @@ sp24_status run_orth(const OrthPlan &pl, OrthSrc src, const OrthOut &o, int step
   return last(true);
 }
 
-// Two ranges of this many bytes have one in common.
-bool overlap(const void *a, const void *b, size_t bytes) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return (x < y ? y - x : x - y) < bytes;
+// Buffers as a call sees them, and whether any that it writes shares memory with another.
+struct Span {
+  const void *p;
+  size_t bytes;
+};
+
+bool overlap(const Span &a, const Span &b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x && y && a.bytes && b.bytes && (x < y ? y - x < a.bytes : x - y < b.bytes);
+}
+
+template <size_t N>
+bool overlaps_any(const Span &a, const Span (&others)[N]) {
+  for (const Span &o : others)
+    if (overlap(a, o)) return true;
+  return false;
 }
 
 sp24_status validate_orth(const OrthPlan &pl, int steps, float eps, const void *workspace, size_t workspace_bytes) {
@@ -1451,6 +1463,8 @@ sp24_status sp24_orthogonalize(const float *G, int64_t count, int64_t rows, int6
   if (!empty && (!aligned_to(G, 4) || !aligned_to(out, 2))) return SP24_ERR_MISALIGNED;
   if ((st = check_device()) != SP24_OK) return st;
   if (empty) return SP24_OK;
+  const Span sg = {G, 4 * (size_t)((count - 1) * batch_stride + (rows - 1) * ldg + cols)};
+  if (overlaps_any(Span{workspace, pl.total}, {sg, Span{out, 2 * (size_t)(count * rows * cols)}})) return SP24_ERR_INVALID_ARG;
   OrthSrc src = {};
   src.g = G;
   src.rows = rows;
@@ -1477,9 +1491,13 @@ sp24_status sp24_muon_step(const float *grad, float *momentum, float *W, void *W
     return SP24_ERR_MISALIGNED;
   if ((st = check_device()) != SP24_OK) return st;
   if (empty) return SP24_OK;
-  // The momentum is written while the gradient may have to be read once more.
-  const size_t bytes = (size_t)count * rows * cols * sizeof(float);
-  if (overlap(momentum, grad, bytes) || overlap(momentum, W, bytes)) return SP24_ERR_INVALID_ARG;
+  // The momentum is written while the gradient may have to be read once more; W16 while other tiles of W still
+  // wait for their update.
+  const size_t n = (size_t)count * rows * cols;
+  const Span sg = {grad, 4 * n}, sm = {momentum, 4 * n}, sw = {W, 4 * n}, s16 = {W16, 2 * n};
+  if (overlaps_any(sm, {sg, sw, s16}) || overlaps_any(s16, {sg, sw}) ||
+      overlaps_any(Span{workspace, pl.total}, {sg, sm, sw, s16}))
+    return SP24_ERR_INVALID_ARG;
   OrthSrc src = {};
   src.g = grad;
   src.m = momentum;
@@ -1508,6 +1526,9 @@ sp24_status sp24_quantize_rows(const void *X, sp24_dtype dtype, int64_t rows, in
   sp24_status st = check_device();
   if (st != SP24_OK) return st;
   if (rows == 0) return SP24_OK;
+  const Span sx = {X, cols ? 2 * (size_t)((rows - 1) * ldx + cols) : 0}, si = {idx, (size_t)(rows / 4) * (size_t)(cols / 4)};
+  const Span sq = {q, (size_t)(rows * cols)}, ss = {scale, 4 * (size_t)rows};
+  if (overlaps_any(sq, {sx, si, ss}) || overlaps_any(ss, {sx, si})) return SP24_ERR_INVALID_ARG;
   const uint16_t *x = static_cast<const uint16_t *>(X);
   return dtype == SP24_BF16 ? launch_quant<true>(x, rows, cols, ldx, idx, q, scale, as_stream(stream))
                             : launch_quant<false>(x, rows, cols, ldx, idx, q, scale, as_stream(stream));
@@ -1524,6 +1545,9 @@ sp24_status sp24_gemm_i8(const int8_t *Xq, const float *sx, int64_t T, int64_t K
   sp24_status st = check_device();
   if (st != SP24_OK) return st;
   if (T == 0) return SP24_OK;
+  if (overlaps_any(Span{Y, 2 * (size_t)(T * N)}, {Span{Xq, (size_t)(T * K)}, Span{Wq, (size_t)(N * K)}, Span{sx, 4 * (size_t)T},
+                                                  Span{sw, 4 * (size_t)N}}))
+    return SP24_ERR_INVALID_ARG;
   cudaStream_t s = as_stream(stream);
   if (dtype == SP24_BF16)
     return epi == SP24_EPI_GELU ? launch_i8<true, true>(Xq, T, K, Wq, N, Y, sx, sw, s)
