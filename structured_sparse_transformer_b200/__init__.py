@@ -499,7 +499,10 @@ def _out_code(t, name: str) -> int:
 
 
 def _expect_rows(t, name, numel, cols):
-    """As _expect, for a 16-bit result: a flat buffer, or rows of `cols` entries."""
+    """As _expect, for a matrix of the caller's: a flat buffer, or rows of `cols` entries (a transposed one of the
+    same size would hold other entries)."""
+    if t is None:
+        return
     _expect(t, name, t.dtype, numel)
     if t.dim() > 1 and t.shape[-1] != cols:
         raise ValueError(f"{name}: expected rows of {cols} entries, got shape {tuple(t.shape)}")
@@ -566,8 +569,10 @@ def sp24_quantize_rows(X, q, scale, idx=None, stream=None):
     R, C = X.shape
     code = _dtype_code(X)
     _expect(q, "q", torch.int8, R * C)
+    _expect_rows(q, "q", R * C, C)
     _expect(scale, "scale", torch.float32, R)
     _expect(idx, "idx", torch.uint8, (R // 4) * (C // 4))
+    _expect_rows(idx, "idx", (R // 4) * (C // 4), C // 4)
     _call_on(_one_device(X, q, scale, idx), "sp24_quantize_rows", stream, X.data_ptr(), code, R, C,
              X.stride(0) if R > 1 else C, None if idx is None else idx.data_ptr(), q.data_ptr(), scale.data_ptr())
 
@@ -588,8 +593,8 @@ def sp24_gemm_i8(Xq, sx, Wq, sw, Y, epi=None, stream=None):
     _expect(sx, "sx", torch.float32, T)
     _expect(sw, "sw", torch.float32, N)
     code = _out_code(Y, "Y")
-    if Y.numel() < T * N:
-        _expect(Y, "Y", Y.dtype, T * N)
+    if Y.numel() < T * N or Y.dim() != 2 or Y.shape[1] != N:
+        _expect_rows(Y, "Y", T * N, N)
     _call_on(_one_device(Xq, sx, Wq, sw, Y), "sp24_gemm_i8", stream, Xq.data_ptr(), sx.data_ptr(), T, K, Wq.data_ptr(),
              sw.data_ptr(), N, code, Y.data_ptr(), EPILOGUES[epi])
 

@@ -38,3 +38,23 @@ def test_scales_at_word_addresses_are_taken():
     if torch.cuda.is_available():
         pytest.skip("a device is present")
     assert _i8(sx=_off(A[1], 4), sw=_off(A[3], 8)) == _quant(scale=_off(A[2], 12)) == E["SP24_ERR_NO_DEVICE"]
+
+
+def test_matrices_of_other_rows_are_refused():
+    """Right in size, but of other rows: a transposed result would hold other entries, a transposed mask prune others.
+    Flat buffers, and more rows than needed, are taken (and stop at the device check)."""
+    T, K, N = 32, 16, 64
+    xq, wq = torch.zeros(T, K, dtype=torch.int8), torch.zeros(N, K, dtype=torch.int8)
+    for shape, why in (((N, T), "rows of 64"), ((1, N, T), "rows of 64"), ((T * N // 16, 16), "rows of 64"),
+                       ((T * N,), "CUDA"), ((T + 2, N), "CUDA"), ((2, T // 2, N), "CUDA"), ((T, N), "CUDA")):
+        with pytest.raises(ValueError, match=why):
+            sp.sp24_gemm_i8(xq, torch.zeros(T), wq, torch.zeros(N), torch.zeros(shape, dtype=torch.float16))
+    R, C = 32, 64
+    x, s = torch.zeros(R, C, dtype=torch.float16), torch.zeros(R)
+    for shape, why in (((C, R), "q: expected rows of 64"), ((R * C,), "CUDA"), ((R + 1, C), "CUDA")):
+        with pytest.raises(ValueError, match=why):
+            sp.sp24_quantize_rows(x, torch.zeros(shape, dtype=torch.int8), s)
+    q = torch.zeros(R, C, dtype=torch.int8)
+    for shape, why in (((C // 4, R // 4), "idx: expected rows of 16"), ((R * C // 16,), "CUDA"), ((R // 4, C // 4), "CUDA")):
+        with pytest.raises(ValueError, match=why):
+            sp.sp24_quantize_rows(x, q, s, torch.zeros(shape, dtype=torch.uint8))
