@@ -593,7 +593,7 @@ def sp24_gemm_i8(Xq, sx, Wq, sw, Y, epi=None, stream=None):
     _expect(sx, "sx", torch.float32, T)
     _expect(sw, "sw", torch.float32, N)
     code = _out_code(Y, "Y")
-    if Y.numel() < T * N or Y.dim() != 2 or Y.shape[1] != N:
+    if Y.shape != (T, N):
         _expect_rows(Y, "Y", T * N, N)
     _call_on(_one_device(Xq, sx, Wq, sw, Y), "sp24_gemm_i8", stream, Xq.data_ptr(), sx.data_ptr(), T, K, Wq.data_ptr(),
              sw.data_ptr(), N, code, Y.data_ptr(), EPILOGUES[epi])
