@@ -410,13 +410,17 @@ SP24_API sp24_status sp24_flip_rate(const uint8_t *idx_prev, const uint8_t *idx_
  *        contents do not matter and are not kept.  One call uses it at a time:
  *        calls that may overlap (streams, graphs replayed side by side) take
  *        one each.
- * Any rows, cols >= 0, the shorter one at most 65536; a zero-sized call does
- * nothing.  A zero matrix gives zeros; a NaN or infinity anywhere in a matrix
- * makes its whole result NaN.  The norm is summed in fp64; the iterates are fp16
- * (scaled by a power of two near sqrt of the longer side) with fp32
+ * Any rows, cols >= 0, the shorter one at most 65536, the longer one at most 2^24,
+ * count at most 65535, and at most 2^30 tiles of 256 x 256 over the stack (others:
+ * SP24_ERR_UNSUPPORTED_SHAPE); a zero-sized call does nothing.  A zero matrix gives
+ * zeros; a NaN or infinity anywhere in a matrix makes its whole result NaN.  The
+ * norm is summed in fp64; the iterates are fp16 (scaled by a power of two near
+ * sqrt of the longer side) with fp32
  * accumulation, about 1e-3 relative error of the result for gradients whose
  * large singular directions do not dwarf the others (the error grows in
- * proportion to |G|_2 over the typical entry of the rest).
+ * proportion to |G|_2 over the typical entry of the rest, and by about 3e-4 a
+ * round beyond the fifth: the iteration has no stable fixed point, and a single
+ * singular value may then end at another place of its band).
  * G and out need only their types' alignment (a matrix of a stack of any size).
  * The workspace overlaps neither of them (refused).
  */

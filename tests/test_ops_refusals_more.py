@@ -58,3 +58,14 @@ def test_matrices_of_other_rows_are_refused():
     for shape, why in (((C // 4, R // 4), "idx: expected rows of 16"), ((R * C // 16,), "CUDA"), ((R // 4, C // 4), "CUDA")):
         with pytest.raises(ValueError, match=why):
             sp.sp24_quantize_rows(x, q, s, torch.zeros(shape, dtype=torch.uint8))
+
+
+def test_the_largest_sizes():
+    """The limits that the header names, just inside and just past them."""
+    def size(count, rows, cols):
+        return _raw("sp24_orthogonalize_size", count, rows, cols, ctypes.byref(ctypes.c_size_t(0)))
+
+    for inside in ((1, 1 << 24, 4), (1, 4, 1 << 24), (1, 65536, 1 << 24), (65535, 4, 4), (65535, 8192, 4096), (1, 65536, 65536)):
+        assert size(*inside) == E["SP24_OK"], inside
+    for past in ((1, (1 << 24) + 1, 4), (1, 4, (1 << 24) + 1), (65536, 4, 4), (1, 65537, 65537), (65535, 65536, 65536)):
+        assert size(*past) == E["SP24_ERR_UNSUPPORTED_SHAPE"], past
