@@ -15,8 +15,8 @@
 // is bounded.
 //
 // Bound by the tensor cores: 32768 x 6400 x 1600 in 227-277 us (2.4-3.0 POP/s, by the box's power),
-// 2047 x 1024 x 4096 with GELU in 14.4 us (its epilogue's 4 us a tile against 3 us of stages).  At
-// 8192 tokens the tensor pipe is busy 68% of 62 us; DRAM reads are the operands once.
+// 2047 x 1024 x 4096 with GELU in 14.2 us (its epilogue's 4 us a tile against 3 us of stages).  At
+// 8192 tokens the tensor pipe is busy 68% of 63 us; DRAM reads are the operands once.
 #pragma once
 #include "gemm_sp.cuh"
 #include "sp24_ops.cuh"
@@ -266,12 +266,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
 
 // ------------------------------------------------------------------ few tokens
 // Where the 256-feature tiles above would leave most pairs idle and K is long: bound by reading Wq
-// and by latency, so K is spread too.  A cluster of S CTAs
-// (S = 1, 2, 4 or 8) computes 128 features x TP tokens, each CTA an S-th of K: M = 128, N = TP
-// MMAs (cta_group::1) on tiles that one thread loads as fast as the ring of stages takes them.  The 32-bit integer partial sums
-// meet through distributed shared memory: each CTA leaves its own in shared memory, and CTA r
-// adds all of them for tokens r, r + S, ..., scales and stores (integer sums: the order does
-// not matter).
+// and by latency, so K is spread too.  A cluster of S CTAs (S = 1, 2, 4 or 8) computes 128
+// features x TP tokens, each CTA an S-th of K: M = 128, N = TP MMAs (cta_group::1) on tiles that
+// a warp (one elected lane issues) loads as fast as the ring of stages takes them.  The 32-bit
+// integer partial sums meet through distributed shared memory: each CTA leaves its own in shared
+// memory, and CTA r adds all of them for tokens r, r + S, ..., scales and stores (integer sums:
+// the order does not matter).
 // At T = 37, K = 5120, N = 1280: 6.7 us, where the pairs' five tiles would take 15.
 constexpr int kI8sThreads = 64 + 256;                  // producer, MMA, eight epilogue warps
 constexpr int kI8sMaxStages = 8;

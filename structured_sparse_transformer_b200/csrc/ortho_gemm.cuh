@@ -11,7 +11,7 @@
 // tiles, fp16 operands, fp32 accumulation) that runs all other phases one after another.  A
 // phase needs everything the one before wrote, so at its end every CTA counts up a counter of
 // the phase once its epilogue warps' stores are complete, and every TMA producer waits for the
-// count: only the producers stall, tensor memory, barriers and descriptors stay set up.
+// count and tells its epilogue warps: tensor memory, barriers and descriptors stay set up.
 // (As 15 launches, each phase paid for launch, set-up and drain: about 9 us each.)  At 1600 x 6400
 // this kernel's 14 phases take 302 us, 240 us of them stages at 0.36-0.40 us; the rest is the
 // exchange of split tiles and the hand-over between phases.
