@@ -391,6 +391,15 @@ __global__ void __launch_bounds__(kI8sThreads)
     // The last MMAs are over before tensor and shared memory go, even if an epilogue gave up waiting for them.
     volatile int no_abort = 0;
     mbar_wait_bounded(over, 0, kDrainBudget, &no_abort);
+    // Tensor memory goes back before this CTA waits for its cluster: another of them may still be waiting for its
+    // own, held by a kernel that in turn waits for what this one holds.
+    if (split > 1) {
+      named_barrier_sync(1, kI8sThreads - 32);   // the epilogue has read it
+      cluster_arrive();
+      tc_fence_after();
+      tmem_dealloc(tmem_base, kCols);
+      cluster_wait();
+    }
   } else if (warp >= 2) {
     // This lane's feature of the tile; the two warps of a lane quadrant take tokens in turn.
     const int q = warp & 3, f = 32 * q + lane, turn = (warp - 2) >> 2;
@@ -439,6 +448,7 @@ __global__ void __launch_bounds__(kI8sThreads)
     }
     tc_fence_before();
     if (split > 1) {
+      named_barrier_arrive(1, kI8sThreads - 32);
       cluster_sync();   // every CTA's sums are in its shared memory
       if (done && f0 + f < N) {
         // kB tokens at a time, four CTAs' words of them in flight together.
@@ -466,16 +476,14 @@ __global__ void __launch_bounds__(kI8sThreads)
     }
   }
   if (split > 1) {
-    if (warp < 2) {
-      __syncwarp();
-      cluster_sync();
-    }
+    __syncwarp();
+    if (warp == 0) cluster_sync();
     __syncwarp();
     cluster_sync();   // no CTA leaves while its sums are read
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == 1 && split == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, kCols);
   }

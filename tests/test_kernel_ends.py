@@ -36,3 +36,13 @@ def test_the_issuing_warp_waits_for_its_last_mmas(file, kernel, pair):
 def test_a_pair_that_gave_up_pauses_before_it_ends(file, kernel):
     tail = _body(file, kernel)[-500:]
     assert re.search(r"__syncthreads\(\);\s*pair_abort_pause\(s_abort\);\s*cluster_sync\(\);", tail)
+
+
+def test_no_tensor_memory_is_held_across_a_clusters_wait():
+    """A cluster whose CTAs need tensor memory one by one: one that holds it and waits for the others, while another kernel's
+    CTAs hold theirs and wait for it, would wait for good.  It is given back before the first wait of the cluster.  (The
+    CTA pairs of the other kernels hold it together: their shared memory leaves no room beside them on an SM.)"""
+    body = _body("gemm_i8.cuh", "gemm_i8_few_kernel")
+    issuer = body[body.index("else if (warp == 1"):body.index("else if (warp >= 2")]
+    assert "cluster_sync()" not in issuer and issuer.index("tmem_dealloc(") < issuer.index("cluster_wait()")
+    assert body.count("tmem_dealloc(") == 2 and "if (warp == 1 && split == 1)" in body
